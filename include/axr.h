@@ -264,6 +264,124 @@ int axr_select_signs(const void *K, int kdtype, const void *q, int qdtype, int64
                      int32_t *best, axr_stream stream);
 
 /*
+ * Attention over whole prompts, causal, with grouped heads and packed sequences
+ * of different lengths: the step before a prompt's keys are quantized into the
+ * cache (the pages start at the cache; this is the standard attention of the
+ * unquantized keys, at the temperature the read path uses).  Sequence s has the
+ * queries cu_q[s] .. cu_q[s+1]-1 and the keys cu_k[s] .. cu_k[s+1]-1; with nq and
+ * nk of them, query i (0-based) sees the keys 0 .. i + nk - nq of its sequence
+ * (the last query sees them all; nk > nq continues an earlier prompt whose keys
+ * come first; where nk < nq the first nq - nk queries see none):
+ *   p = softmax over those keys j of q_i . k_j / sqrt(d)
+ *   out_i = sum_j p_j V_j,   lse_i = log sum_j exp(q_i . k_j / sqrt(d)).
+ * A query that sees no key gets out = 0 and lse = -inf.  Rows of q that belong to
+ * no sequence leave out and lse as they were.
+ *
+ * q        device, heads*group x total_q rows of d elements of dtype; query head
+ *          h*group + g reads KV head h.
+ * K, V     device, heads x total_k rows of d elements of dtype.
+ * cu_q     device int32[batch + 1], non-decreasing, within [0, total_q];
+ * cu_k     the same for the keys, within [0, total_k].  (Values outside, or
+ *          decreasing ones, give undefined rows of out and lse and no access
+ *          outside the buffers.)
+ * strides  HOST int64[8], read before the call returns: elements between heads
+ *          and between rows of q, of K, of V and of out, in this order.  Rows
+ *          are contiguous; all strides are >= 0 and multiples of 16 bytes.  Row
+ *          strides are >= d.
+ * out      device, heads*group x total_q rows of d elements of dtype; must not
+ *          overlap the inputs.
+ * lse      device float[(heads*group) * total_q], or NULL.
+ * q, K, V, out 16-byte aligned.  d a power of two in [32, 512]; group in [1, 8];
+ * total_q, total_k at most 2^31 - 1; at most 65535 query heads.  total_q == 0 or batch == 0 is a
+ * no-op.  The products are exact or accumulated in fp32, the softmax is fp32;
+ * for 16-bit types with d = 64, 128 and 256 the weights p are rounded to dtype
+ * for the product with V.  One kernel on `stream`, no workspace.
+ */
+int axr_prompt_attention(const void *q, const void *K, const void *V, int dtype, int64_t total_q, int64_t total_k,
+                         const int32_t *cu_q, const int32_t *cu_k, int batch, int heads, int group, int d,
+                         const int64_t *strides, void *out, float *lse, axr_stream stream);
+
+/*
+ * Decode attention of a batch whose sequences share a prefix: one query per query
+ * head of every sequence, over the prefix's quantized keys, stored once, and then
+ * the sequence's own quantized keys (the tokens generated since).  The prefix is
+ * read once for the whole batch.  For query head h*group + g of sequence s,
+ *   p = softmax over the n prefix keys of KV head h and the first lengths[s]
+ *       rows of cache s*heads + h, of the scores axr_scores defines
+ *   out = sum p_t V_t,   lse = log sum_t exp(score_t).
+ * With neither prefix nor own keys out = 0 and lse = -inf.
+ *
+ * q             device, (batch*heads*group) x d row-major of qdtype, row
+ *               (s*heads + h)*group + g; 16-byte aligned.
+ * prefix_idx, prefix_norms, prefix_V   device, heads x n rows of packed codes,
+ *               norms and values (vdtype), as axr_attention reads them; n >= 0.
+ * idx, norms, V device, (batch*heads) x capacity rows: every sequence's own
+ *               cache, as axr_append_scores lays it out; capacity >= 0.  Rows from
+ *               lengths[s] on are not used, whatever they hold.
+ * lengths       device int32[batch], own keys of each sequence, in [0, capacity]
+ *               (others are clamped).
+ * signs         device int8[d], the pattern all keys were written with.
+ * workspace     device scratch of at least axr_attention_shared_workspace_bytes
+ *               bytes, 256-byte aligned; contents do not matter on entry and are
+ *               unspecified on exit.  Calls that share a workspace must not overlap.
+ * out           device, (batch*heads*group) x d of vdtype; 16-byte aligned.
+ * lse           device float[batch*heads*group], or NULL.
+ * Codes and V 16-byte aligned, norms 4-byte (either set may be NULL when its n or
+ * capacity is 0).  d a power of two in [32, 512]; b in [1, 4]; group in [1, 8];
+ * n and capacity at most 2^31 - 129; at most 2^31 - 1 query rows.  Sums and softmax are
+ * fp32; out is rounded to vdtype once.  Three kernels on `stream`.
+ */
+int axr_attention_shared_workspace_bytes(int batch, int heads, int group, int d, int64_t *bytes);
+int axr_attention_shared(const void *q, int qdtype, const uint8_t *prefix_idx, const float *prefix_norms,
+                         const void *prefix_V, int64_t n, const uint8_t *idx, const float *norms, const void *V,
+                         int64_t capacity, const int32_t *lengths, int vdtype, int batch, int heads, int group, int d,
+                         int b, const int8_t *signs, void *workspace, int64_t workspace_bytes, void *out, float *lse,
+                         axr_stream stream);
+
+/*
+ * Accumulated attention weight of cached keys: adds one decode step's softmax
+ * weights, summed over the query heads of each KV head, to the running sums that
+ * axr_evict chooses by.  For KV head h and t < lengths[h] (n if lengths is NULL)
+ *   weights[h, t] += sum_g softmax over t' < lengths[h] of scores[h*group + g, t'], at t.
+ * A row of scores that is -inf throughout adds nothing.  Entries from lengths[h]
+ * on are left as they were.
+ *
+ * scores   device float[(heads*group) * n], as axr_append_scores and
+ *          axr_attention return them (row stride n); 4-byte aligned.
+ * weights  device float[heads * capacity], capacity >= n; 4-byte aligned.
+ * lengths  device int32[heads], in [0, n] (others are clamped), or NULL.
+ * group in [1, 8]; n and capacity at most 2^31 - 1; n == 0 is a no-op.
+ * One kernel on `stream`; sums run in a fixed order.
+ */
+int axr_accumulate_weights(const float *scores, int64_t n, int heads, int group, const int32_t *lengths,
+                           float *weights, int64_t capacity, axr_stream stream);
+
+/*
+ * Eviction by accumulated attention weight: shrinks every head's cache to at most
+ * `keep` rows.  The newest `recent` rows of a head stay, and of its older rows the
+ * keep - recent of largest weight (of equal weights the lower row; a NaN counts
+ * as lowest).  Rows that stay keep their order and are copied to a second cache
+ * with their norms, values and weights; a head with at most `keep` rows keeps all.
+ *
+ * idx, norms, V  device, heads x capacity rows: the cache (V of vdtype).
+ * weights        device float[heads * capacity].
+ * lengths        device int32[heads]: rows in use, in [0, capacity] (others are clamped).
+ * idx_out, norms_out, V_out, weights_out   device, heads x capacity_out rows,
+ *                capacity_out >= keep: rows from the new length on are left as
+ *                they were.  None may overlap an input.
+ * kept           device int32[heads * keep], written: the source row of each row
+ *                that stays, ascending; -1 from the new length on.
+ * lengths_out    device int32[heads], written: min(lengths[h], keep).
+ * idx, V, idx_out, V_out 16-byte aligned, the rest 4-byte.  d a power of two in
+ * [8, 512]; b in [1, 4]; 0 <= recent <= keep, keep >= 1; capacities at most
+ * 2^31 - 1; at most 65535 heads.  capacity == 0 is allowed.  Two kernels on `stream`, no workspace.
+ */
+int axr_evict(const uint8_t *idx, const float *norms, const void *V, int vdtype, const float *weights,
+              const int32_t *lengths, int64_t capacity, int64_t keep, int64_t recent, int heads, int d, int b,
+              uint8_t *idx_out, float *norms_out, void *V_out, float *weights_out, int64_t capacity_out,
+              int32_t *kept, int32_t *lengths_out, axr_stream stream);
+
+/*
  * Device-side status of the kernels (no counterpart in the method; a
  * diagnostic).  Every wait inside the tensor-core kernels is bounded; a wait that
  * runs out records a bit here instead of hanging: 1 = a tile load never arrived,

@@ -7,14 +7,19 @@ load the library; the first call does, and raises if it has not been built.
 """
 from .axr import (  # noqa: F401
     AxrError,
+    axr_accumulate_weights,
     axr_append_scores,
     axr_attention,
+    axr_attention_shared,
+    axr_attention_shared_workspace_bytes,
     axr_attention_static,
     axr_attention_workspace_bytes,
     axr_debug_build,
     axr_debug_set_span_slack,
     axr_device_status,
+    axr_evict,
     axr_make_codebook,
+    axr_prompt_attention,
     axr_quantize_keys,
     axr_quantize_keys_block,
     axr_scores,
@@ -26,14 +31,19 @@ from .axr import (  # noqa: F401
 
 __all__ = [
     "AxrError",
+    "axr_accumulate_weights",
     "axr_append_scores",
     "axr_attention",
+    "axr_attention_shared",
+    "axr_attention_shared_workspace_bytes",
     "axr_attention_static",
     "axr_attention_workspace_bytes",
     "axr_debug_build",
     "axr_debug_set_span_slack",
     "axr_device_status",
+    "axr_evict",
     "axr_make_codebook",
+    "axr_prompt_attention",
     "axr_quantize_keys",
     "axr_quantize_keys_block",
     "axr_scores",

@@ -36,6 +36,13 @@ SIGNATURES = {
     "axr_quantize_keys_block": (_I32, [_P, _I32, _I64, _I32, _I32, _P, _P, _P, _P]),
     "axr_scores_block": (_I32, [_P, _I32, _P, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, _P]),
     "axr_select_signs": (_I32, [_P, _I32, _P, _I32, _I64, _I32, _I32, _I32, _I32, _I32, _P, _I32, _P, _P, _P]),
+    "axr_prompt_attention": (_I32, [_P, _P, _P, _I32, _I64, _I64, _P, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P]),
+    "axr_attention_shared_workspace_bytes": (_I32, [_I32, _I32, _I32, _I32, _P]),
+    "axr_attention_shared": (_I32, [_P, _I32, _P, _P, _P, _I64, _P, _P, _P, _I64, _P, _I32, _I32, _I32, _I32, _I32,
+                                    _I32, _P, _P, _I64, _P, _P, _P]),
+    "axr_accumulate_weights": (_I32, [_P, _I64, _I32, _I32, _P, _P, _I64, _P]),
+    "axr_evict": (_I32, [_P, _P, _P, _I32, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32, _P, _P, _P, _P, _I64, _P, _P,
+                         _P]),
     "axr_status_string": (ctypes.c_char_p, [_I32]),
     "axr_last_error": (ctypes.c_char_p, []),
     "axr_version": (_I32, []),
@@ -400,6 +407,208 @@ def axr_select_signs(K: torch.Tensor, q: torch.Tensor, group: int, b: int, candi
           K.data_ptr(), _DTYPE_CODE[K.dtype], q.data_ptr(), _DTYPE_CODE[q.dtype], n, samples, heads, group, d,
           b, candidates.data_ptr(), C, errors.data_ptr(), best.data_ptr())
     return errors, best
+
+
+def _require_rows(t: torch.Tensor, name: str) -> None:
+    """A CUDA tensor (heads, rows, d) whose rows are contiguous; heads and rows may be strided."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (libaxr has no CPU path)")
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be (heads, rows, d) with contiguous rows")
+
+
+def _row_strides(t: torch.Tensor) -> tuple[int, int]:
+    """Element strides of heads and rows; those of an axis of length 1 are free and
+    are given as a dense tensor has them."""
+    rows, d = t.shape[1], t.shape[2]
+    row = t.stride(1) if rows > 1 else d
+    return (t.stride(0) if t.shape[0] > 1 else rows * row), row
+
+
+def _check_int32(t: torch.Tensor, name: str, count: int) -> None:
+    _require_cuda(t, name)
+    if t.dtype != torch.int32 or t.numel() != count:
+        raise ValueError(f"{name} must be int32 with {count} entries")
+
+
+def axr_prompt_attention(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: torch.Tensor,
+                         cu_k: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                         lse: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Causal attention over packed prompts: queries q (heads*group, total_q, d), keys
+    and values K, V (heads, total_k, d), all of one dtype; heads and rows may be
+    strided (a token-major tensor transposed).  Sequence s has the queries
+    cu_q[s] .. cu_q[s+1]-1 and the keys cu_k[s] .. cu_k[s+1]-1 (cu_k defaults to
+    cu_q), the last query seeing the last key.  Returns (out like q, lse
+    (heads*group, total_q) fp32); rows of no sequence are not written."""
+    for t, name in ((q, "q"), (K, "K"), (V, "V")):
+        _require_rows(t, name)
+        if t.dtype not in _DTYPE_CODE or t.dtype != q.dtype:
+            raise ValueError("q, K and V must share a dtype: float32, float16 or bfloat16")
+    hq, total_q, d = q.shape
+    heads, total_k = K.shape[:2]
+    if tuple(V.shape) != tuple(K.shape) or K.shape[2] != d:
+        raise ValueError(f"K and V must both be (heads, total_k, {d})")
+    if heads < 1 or hq % heads:
+        raise ValueError("q must have heads*group heads")
+    if cu_k is None:
+        cu_k = cu_q
+    batch = cu_q.numel() - 1
+    if batch < 0:
+        raise ValueError("cu_q must have batch + 1 entries")
+    _check_int32(cu_q, "cu_q", batch + 1)
+    _check_int32(cu_k, "cu_k", batch + 1)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((hq, total_q), dtype=torch.float32, device=q.device)
+    _require_rows(out, "out")
+    _require_cuda(lse, "lse")
+    if out.dtype != q.dtype or tuple(out.shape) != tuple(q.shape) or lse.dtype != torch.float32 \
+            or lse.numel() < hq * total_q:
+        raise ValueError("out must be like q and lse float32 with heads*group*total_q elements")
+    strides = (ctypes.c_int64 * 8)(*_row_strides(q), *_row_strides(K), *_row_strides(V), *_row_strides(out))
+    _call("axr_prompt_attention", q.device, stream,
+          q.data_ptr(), K.data_ptr(), V.data_ptr(), _DTYPE_CODE[q.dtype], total_q, total_k, cu_q.data_ptr(),
+          cu_k.data_ptr(), batch, heads, hq // heads, d, ctypes.addressof(strides), out.data_ptr(), lse.data_ptr())
+    return out, lse
+
+
+def axr_attention_shared_workspace_bytes(batch: int, heads: int, group: int, d: int) -> int:
+    """Scratch bytes axr_attention_shared needs for this shape on the current device."""
+    out = ctypes.c_int64(0)
+    _raise(library().axr_attention_shared_workspace_bytes(batch, heads, group, d, ctypes.byref(out)),
+           "axr_attention_shared_workspace_bytes")
+    return out.value
+
+
+def axr_attention_shared(q: torch.Tensor, prefix_idx: torch.Tensor, prefix_norms: torch.Tensor,
+                         prefix_V: torch.Tensor, idx: torch.Tensor, norms: torch.Tensor, V: torch.Tensor,
+                         lengths: torch.Tensor, group: int, b: int, signs: torch.Tensor,
+                         workspace: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                         lse: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Decode attention of a batch over a shared prefix and each sequence's own keys:
+    q (batch*heads*group, d); the prefix prefix_idx (heads, n, d*b/8), prefix_norms
+    (heads, n), prefix_V (heads, n, d); the own caches idx (batch*heads, capacity,
+    d*b/8), norms (batch*heads, capacity), V (batch*heads, capacity, d), of which
+    the first lengths[s] (int32 (batch)) rows of sequence s are used.  Returns
+    (out (batch*heads*group, d) in V's dtype, lse (batch*heads*group) fp32)."""
+    for t, name in ((q, "q"), (prefix_idx, "prefix_idx"), (prefix_norms, "prefix_norms"), (prefix_V, "prefix_V"),
+                    (idx, "idx"), (norms, "norms"), (V, "V"), (signs, "signs")):
+        _require_cuda(t, name)
+    if q.dtype not in _DTYPE_CODE or V.dtype not in _DTYPE_CODE or prefix_V.dtype != V.dtype:
+        raise ValueError("q and V must be float32, float16 or bfloat16, prefix_V of V's dtype")
+    _check_read_operands(prefix_idx, prefix_norms)
+    _check_read_operands(idx, norms)
+    rows, d = q.shape
+    _check_signs(signs, d)
+    P = packed_row_bytes(d, b)
+    if prefix_idx.dim() != 3 or prefix_idx.shape[0] < 1 or prefix_idx.shape[2] != P:
+        raise ValueError(f"prefix_idx must be (heads, n, {P})")
+    heads, n = prefix_idx.shape[:2]
+    if group < 1 or rows % (heads * group):
+        raise ValueError("q must have batch*heads*group rows")
+    batch = rows // (heads * group)
+    if tuple(prefix_norms.shape) != (heads, n) or tuple(prefix_V.shape) != (heads, n, d):
+        raise ValueError(f"prefix_norms must be ({heads}, {n}) and prefix_V ({heads}, {n}, {d})")
+    if idx.dim() != 3 or idx.shape[0] != batch * heads or idx.shape[2] != P:
+        raise ValueError(f"idx must be (batch*heads={batch * heads}, capacity, {P})")
+    capacity = idx.shape[1]
+    if tuple(norms.shape) != (batch * heads, capacity) or tuple(V.shape) != (batch * heads, capacity, d):
+        raise ValueError(f"norms must be ({batch * heads}, {capacity}) and V ({batch * heads}, {capacity}, {d})")
+    _check_int32(lengths, "lengths", batch)
+    if out is None:
+        out = torch.empty((rows, d), dtype=V.dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty(rows, dtype=torch.float32, device=q.device)
+    if workspace is None:
+        with torch.cuda.device(q.device):
+            need = axr_attention_shared_workspace_bytes(batch, heads, group, d)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    for t, name in ((out, "out"), (lse, "lse"), (workspace, "workspace")):
+        _require_cuda(t, name)
+    if out.dtype != V.dtype or out.numel() < rows * d or lse.dtype != torch.float32 or lse.numel() < rows:
+        raise ValueError("out must be of V's dtype and lse float32, both large enough")
+    _call("axr_attention_shared", q.device, stream,
+          q.data_ptr(), _DTYPE_CODE[q.dtype], prefix_idx.data_ptr(), prefix_norms.data_ptr(), prefix_V.data_ptr(), n,
+          idx.data_ptr(), norms.data_ptr(), V.data_ptr(), capacity, lengths.data_ptr(), _DTYPE_CODE[V.dtype], batch,
+          heads, group, d, b, signs.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+          out.data_ptr(), lse.data_ptr())
+    return out, lse
+
+
+def axr_accumulate_weights(scores: torch.Tensor, weights: torch.Tensor, group: int,
+                           lengths: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Add a decode step's softmax weights to the running sums of the cached keys:
+    weights (heads, capacity)[h, t] += sum over the head's queries of the softmax of
+    scores (heads*group, n) over the first lengths[h] (int32 (heads); default n)
+    keys.  Returns weights."""
+    _require_cuda(scores, "scores")
+    _require_cuda(weights, "weights")
+    if scores.dtype != torch.float32 or weights.dtype != torch.float32 or scores.dim() != 2 or weights.dim() != 2:
+        raise ValueError("scores and weights must be 2-D float32 tensors")
+    heads, capacity = weights.shape
+    n = scores.shape[1]
+    if group < 1 or scores.shape[0] != heads * group or capacity < n:
+        raise ValueError(f"scores must be ({heads}*{group}, n) with n at most {capacity}")
+    if lengths is not None:
+        _check_int32(lengths, "lengths", heads)
+    _call("axr_accumulate_weights", scores.device, stream,
+          scores.data_ptr(), n, heads, group, lengths.data_ptr() if lengths is not None else None,
+          weights.data_ptr(), capacity)
+    return weights
+
+
+def axr_evict(idx: torch.Tensor, norms: torch.Tensor, V: torch.Tensor, weights: torch.Tensor, lengths: torch.Tensor,
+              keep: int, recent: int, out: tuple | None = None, stream=None) -> tuple[torch.Tensor, ...]:
+    """Shrink a cache to at most ``keep`` rows a head by accumulated attention weight:
+    idx (heads, capacity, d*b/8), norms (heads, capacity), V (heads, capacity, d),
+    weights (heads, capacity), rows in use lengths (int32 (heads)).  The newest
+    ``recent`` rows stay, and the keep - recent older ones of largest weight.
+    Returns (idx, norms, V, weights, kept, lengths): a second cache of keep rows a
+    head, the int32 (heads, keep) source rows (-1 past the new length) and the new
+    lengths.  ``out`` gives these six tensors; its cache may hold more rows a head."""
+    for t, name in ((idx, "idx"), (norms, "norms"), (V, "V"), (weights, "weights")):
+        _require_cuda(t, name)
+    _check_read_operands(idx, norms)
+    if V.dtype not in _DTYPE_CODE or weights.dtype != torch.float32:
+        raise ValueError("V must be float32, float16 or bfloat16, weights float32")
+    if V.dim() != 3 or idx.dim() != 3:
+        raise ValueError("V must be (heads, capacity, d) and idx (heads, capacity, d*b/8)")
+    heads, capacity, d = V.shape
+    P = idx.shape[2]
+    b = P * 8 // d if d else 0
+    if tuple(idx.shape) != (heads, capacity, packed_row_bytes(d, b)) or tuple(norms.shape) != (heads, capacity) \
+            or tuple(weights.shape) != (heads, capacity):
+        raise ValueError(f"idx must be ({heads}, {capacity}, d*b/8), norms and weights ({heads}, {capacity})")
+    _check_int32(lengths, "lengths", heads)
+    if not 0 <= recent <= keep or keep < 1:
+        raise ValueError(f"keep={keep}, recent={recent}: needs keep >= 1 and 0 <= recent <= keep")
+    dev = V.device
+    if out is None:
+        out = (torch.empty((heads, keep, P), dtype=torch.uint8, device=dev),
+               torch.empty((heads, keep), dtype=torch.float32, device=dev),
+               torch.empty((heads, keep, d), dtype=V.dtype, device=dev),
+               torch.empty((heads, keep), dtype=torch.float32, device=dev),
+               torch.empty((heads, keep), dtype=torch.int32, device=dev),
+               torch.empty(heads, dtype=torch.int32, device=dev))
+    if len(out) != 6:
+        raise ValueError("out must hold idx, norms, V, weights, kept and lengths")
+    for t, name in zip(out, ("idx", "norms", "V", "weights", "kept", "lengths")):
+        _require_cuda(t, f"out's {name}")
+    idx_o, norms_o, V_o, weights_o, kept, lengths_o = out
+    _check_read_operands(idx_o, norms_o)
+    capacity_o = V_o.shape[1] if V_o.dim() == 3 else -1
+    if V_o.dtype != V.dtype or weights_o.dtype != torch.float32 or capacity_o < keep \
+            or tuple(V_o.shape) != (heads, capacity_o, d) or tuple(idx_o.shape) != (heads, capacity_o, P) \
+            or tuple(norms_o.shape) != (heads, capacity_o) or tuple(weights_o.shape) != (heads, capacity_o):
+        raise ValueError("out's cache must be like the input's with at least keep rows a head")
+    _check_int32(kept, "out's kept", heads * keep)
+    _check_int32(lengths_o, "out's lengths", heads)
+    _call("axr_evict", dev, stream,
+          idx.data_ptr(), norms.data_ptr(), V.data_ptr(), _DTYPE_CODE[V.dtype], weights.data_ptr(),
+          lengths.data_ptr(), capacity, keep, recent, heads, d, b, idx_o.data_ptr(), norms_o.data_ptr(),
+          V_o.data_ptr(), weights_o.data_ptr(), capacity_o, kept.data_ptr(), lengths_o.data_ptr())
+    return out
 
 
 def axr_device_status(clear: bool = True) -> int:

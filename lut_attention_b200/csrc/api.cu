@@ -7,6 +7,8 @@
 #include <vector>
 
 #include "axr_internal.cuh"
+#include "prompt.cuh"
+#include "shared.cuh"
 
 namespace axr {
 namespace {
@@ -456,6 +458,201 @@ extern "C" int axr_select_signs(const void *K, int kdtype, const void *q, int qd
     if (!get_codebook(d, b, &a.cb)) return fail(AXR_EUNSUPPORTED, "no codebook for d=%d b=%d", d, b);
     const cudaError_t e = launch_sign_select(a, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(AXR_ECUDA, "sign selection launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+namespace {
+
+int check_heads(int heads, int group)
+{
+    if (heads < 1) return fail(AXR_EINVAL, "heads=%d must be >= 1", heads);
+    if (group < 1) return fail(AXR_EINVAL, "group=%d must be >= 1", group);
+    if (group > kMaxGroup) return fail(AXR_EUNSUPPORTED, "group=%d: at most %d", group, kMaxGroup);
+    return AXR_OK;
+}
+
+// whether two byte ranges share a byte
+bool overlap(const void *a, int64_t na, const void *b, int64_t nb)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return na > 0 && nb > 0 && x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
+}
+
+}  // namespace
+
+extern "C" int axr_prompt_attention(const void *q, const void *K, const void *V, int dtype, int64_t total_q,
+                                    int64_t total_k, const int32_t *cu_q, const int32_t *cu_k, int batch, int heads,
+                                    int group, int d, const int64_t *strides, void *out, float *lse,
+                                    axr_stream stream)
+{
+    int rc;
+    const int es = elem_size(dtype);
+    if (es == 0) return fail(AXR_EINVAL, "dtype=%d is not an axr_dtype", dtype);
+    if (!pow2_in_range(d) || d < 32) return fail(AXR_EUNSUPPORTED, "d=%d: attention needs a power of two in [32, 512]", d);
+    if ((rc = check_heads(heads, group)) != AXR_OK) return rc;
+    if (total_q < 0 || total_k < 0 || batch < 0)
+        return fail(AXR_EINVAL, "total_q, total_k or batch is negative");
+    if (total_q > (int64_t)INT32_MAX || total_k > (int64_t)INT32_MAX)
+        return fail(AXR_EUNSUPPORTED, "at most 2^31-1 packed rows");
+    if ((int64_t)heads * group > 65535) return fail(AXR_EUNSUPPORTED, "%d x %d query heads: at most 65535", heads, group);
+    if (total_q == 0 || batch == 0) return ok();
+    if (!strides) return fail(AXR_EINVAL, "strides is NULL");
+    static const char *const names[4] = {"q", "K", "V", "out"};
+    for (int i = 0; i < 4; ++i) {
+        const int64_t hd = strides[2 * i], row = strides[2 * i + 1];
+        if (hd < 0 || row < d || hd * es % 16 != 0 || row * es % 16 != 0)
+            return fail(AXR_EINVAL, "strides of %s (%lld, %lld): multiples of 16 bytes, rows at least d apart", names[i],
+                        (long long)hd, (long long)row);
+    }
+    if ((rc = check_device_ptr(q, 16, "q")) != AXR_OK) return rc;
+    if (total_k > 0) {
+        if ((rc = check_device_ptr(K, 16, "K")) != AXR_OK) return rc;
+        if ((rc = check_device_ptr(V, 16, "V")) != AXR_OK) return rc;
+    }
+    if ((rc = check_device_ptr(cu_q, 4, "cu_q")) != AXR_OK) return rc;
+    if ((rc = check_device_ptr(cu_k, 4, "cu_k")) != AXR_OK) return rc;
+    if ((rc = check_device_ptr(out, 16, "out")) != AXR_OK) return rc;
+    if (lse && (rc = check_device_ptr(lse, 4, "lse")) != AXR_OK) return rc;
+
+    PromptArgs a{};
+    a.q = q;
+    a.K = K;
+    a.V = V;
+    a.dtype = dtype;
+    a.d = d;
+    a.out = out;
+    a.lse = lse;
+    a.s = PromptShape{cu_q, cu_k, batch, heads, group, (int)total_q, (int)total_k, strides[0], strides[1],
+                      strides[2], strides[3], strides[4], strides[5], strides[6], strides[7]};
+    const cudaError_t e = launch_prompt_attention(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(AXR_ECUDA, "prompt attention launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+extern "C" int axr_attention_shared_workspace_bytes(int batch, int heads, int group, int d, int64_t *bytes)
+{
+    int rc;
+    if (!bytes) return fail(AXR_EINVAL, "bytes is NULL");
+    if (!pow2_in_range(d) || d < 32) return fail(AXR_EUNSUPPORTED, "d=%d: attention needs a power of two in [32, 512]", d);
+    if (batch < 0) return fail(AXR_EINVAL, "batch=%d is negative", batch);
+    if ((rc = check_heads(heads, group)) != AXR_OK) return rc;
+    if ((int64_t)batch * heads > INT32_MAX / group)
+        return fail(AXR_EUNSUPPORTED, "%d x %d x %d query rows: at most 2^31-1", batch, heads, group);
+    *bytes = batch == 0 ? 0 : shared_workspace_bytes(batch, heads, group, d);
+    return ok();
+}
+
+extern "C" int axr_attention_shared(const void *q, int qdtype, const uint8_t *prefix_idx, const float *prefix_norms,
+                                    const void *prefix_V, int64_t n, const uint8_t *idx, const float *norms,
+                                    const void *V, int64_t capacity, const int32_t *lengths, int vdtype, int batch,
+                                    int heads, int group, int d, int b, const int8_t *signs, void *workspace,
+                                    int64_t workspace_bytes, void *out, float *lse, axr_stream stream)
+{
+    int rc = check_shape(d, b);
+    if (rc != AXR_OK) return rc;
+    if (elem_size(qdtype) == 0) return fail(AXR_EINVAL, "qdtype=%d is not an axr_dtype", qdtype);
+    if (elem_size(vdtype) == 0) return fail(AXR_EINVAL, "vdtype=%d is not an axr_dtype", vdtype);
+    if (n < 0) return fail(AXR_EINVAL, "n=%lld is negative", (long long)n);
+    if (capacity < 0) return fail(AXR_EINVAL, "capacity=%lld is negative", (long long)capacity);
+    const int64_t most = (int64_t)INT32_MAX - shared::kTileKeys;
+    if (n > most || capacity > most) return fail(AXR_EUNSUPPORTED, "n or capacity: at most 2^31-129 keys");
+    int64_t need = 0;
+    if ((rc = axr_attention_shared_workspace_bytes(batch, heads, group, d, &need)) != AXR_OK) return rc;
+    if (batch == 0) return ok();
+    if (workspace_bytes < need)
+        return fail(AXR_EINVAL, "workspace_bytes=%lld: needs %lld", (long long)workspace_bytes, (long long)need);
+    if ((rc = check_device_ptr(q, 16, "q")) != AXR_OK) return rc;
+    if (n > 0) {
+        if ((rc = check_device_ptr(prefix_idx, 16, "prefix_idx")) != AXR_OK) return rc;
+        if ((rc = check_device_ptr(prefix_norms, 4, "prefix_norms")) != AXR_OK) return rc;
+        if ((rc = check_device_ptr(prefix_V, 16, "prefix_V")) != AXR_OK) return rc;
+    }
+    if (capacity > 0) {
+        if ((rc = check_device_ptr(idx, 16, "idx")) != AXR_OK) return rc;
+        if ((rc = check_device_ptr(norms, 4, "norms")) != AXR_OK) return rc;
+        if ((rc = check_device_ptr(V, 16, "V")) != AXR_OK) return rc;
+    }
+    if ((rc = check_device_ptr(lengths, 4, "lengths")) != AXR_OK) return rc;
+    if ((rc = check_device_ptr(signs, 1, "signs")) != AXR_OK) return rc;
+    if ((rc = check_device_ptr(workspace, 256, "workspace")) != AXR_OK) return rc;
+    if ((rc = check_device_ptr(out, 16, "out")) != AXR_OK) return rc;
+    if (lse && (rc = check_device_ptr(lse, 4, "lse")) != AXR_OK) return rc;
+
+    SharedArgs a{q, qdtype, prefix_idx, prefix_norms, prefix_V, n, idx, norms, V, capacity, lengths, vdtype, batch,
+                 heads, group, d, b, signs, workspace, out, lse, Codebook{}};
+    if (!get_codebook(d, b, &a.cb)) return fail(AXR_EUNSUPPORTED, "no codebook for d=%d b=%d", d, b);
+    const cudaError_t e = launch_shared_attention(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(AXR_ECUDA, "shared-prefix attention launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+extern "C" int axr_accumulate_weights(const float *scores, int64_t n, int heads, int group, const int32_t *lengths,
+                                      float *weights, int64_t capacity, axr_stream stream)
+{
+    int rc;
+    if (n < 0) return fail(AXR_EINVAL, "n=%lld is negative", (long long)n);
+    if ((rc = check_heads(heads, group)) != AXR_OK) return rc;
+    if (capacity < n) return fail(AXR_EINVAL, "capacity=%lld is below n=%lld", (long long)capacity, (long long)n);
+    if (capacity > (int64_t)INT32_MAX) return fail(AXR_EUNSUPPORTED, "capacity=%lld: at most 2^31-1", (long long)capacity);
+    if (heads > (1 << 27)) return fail(AXR_EUNSUPPORTED, "heads=%d: at most 2^27", heads);
+    if (n == 0) return ok();
+    if ((rc = check_device_ptr(scores, 4, "scores")) != AXR_OK) return rc;
+    if ((rc = check_device_ptr(weights, 4, "weights")) != AXR_OK) return rc;
+    if (lengths && (rc = check_device_ptr(lengths, 4, "lengths")) != AXR_OK) return rc;
+    const WeightArgs a{scores, weights, lengths, n, capacity, heads, group};
+    const cudaError_t e = launch_accumulate_weights(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(AXR_ECUDA, "weight accumulation launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+extern "C" int axr_evict(const uint8_t *idx, const float *norms, const void *V, int vdtype, const float *weights,
+                         const int32_t *lengths, int64_t capacity, int64_t keep, int64_t recent, int heads, int d,
+                         int b, uint8_t *idx_out, float *norms_out, void *V_out, float *weights_out,
+                         int64_t capacity_out, int32_t *kept, int32_t *lengths_out, axr_stream stream)
+{
+    int rc = check_shape(d, b);
+    if (rc != AXR_OK) return rc;
+    const int es = elem_size(vdtype);
+    if (es == 0) return fail(AXR_EINVAL, "vdtype=%d is not an axr_dtype", vdtype);
+    if (heads < 1) return fail(AXR_EINVAL, "heads=%d must be >= 1", heads);
+    if (heads > 65535) return fail(AXR_EUNSUPPORTED, "heads=%d: at most 65535", heads);
+    if (capacity < 0) return fail(AXR_EINVAL, "capacity=%lld is negative", (long long)capacity);
+    if (keep < 1 || recent < 0 || recent > keep)
+        return fail(AXR_EINVAL, "keep=%lld, recent=%lld: needs keep >= 1 and 0 <= recent <= keep", (long long)keep,
+                    (long long)recent);
+    if (capacity_out < keep)
+        return fail(AXR_EINVAL, "capacity_out=%lld is below keep=%lld", (long long)capacity_out, (long long)keep);
+    if (capacity > (int64_t)INT32_MAX || capacity_out > (int64_t)INT32_MAX)
+        return fail(AXR_EUNSUPPORTED, "capacity: at most 2^31-1 rows");
+    if (capacity > 0) {
+        if ((rc = check_device_ptr(idx, 16, "idx")) != AXR_OK) return rc;
+        if ((rc = check_device_ptr(norms, 4, "norms")) != AXR_OK) return rc;
+        if ((rc = check_device_ptr(V, 16, "V")) != AXR_OK) return rc;
+        if ((rc = check_device_ptr(weights, 4, "weights")) != AXR_OK) return rc;
+    }
+    if ((rc = check_device_ptr(lengths, 4, "lengths")) != AXR_OK) return rc;
+    if ((rc = check_device_ptr(idx_out, 16, "idx_out")) != AXR_OK) return rc;
+    if ((rc = check_device_ptr(norms_out, 4, "norms_out")) != AXR_OK) return rc;
+    if ((rc = check_device_ptr(V_out, 16, "V_out")) != AXR_OK) return rc;
+    if ((rc = check_device_ptr(weights_out, 4, "weights_out")) != AXR_OK) return rc;
+    if ((rc = check_device_ptr(kept, 4, "kept")) != AXR_OK) return rc;
+    if ((rc = check_device_ptr(lengths_out, 4, "lengths_out")) != AXR_OK) return rc;
+    const int64_t in_rows = (int64_t)heads * capacity, out_rows = (int64_t)heads * capacity_out;
+    const int64_t pb = (int64_t)d * b / 8, vb = (int64_t)d * es;
+    const struct { const void *p; int64_t bytes; } in[5] = {{idx, in_rows * pb}, {norms, in_rows * 4}, {V, in_rows * vb},
+                                                            {weights, in_rows * 4}, {lengths, (int64_t)heads * 4}},
+        to[6] = {{idx_out, out_rows * pb}, {norms_out, out_rows * 4}, {V_out, out_rows * vb}, {weights_out, out_rows * 4},
+                 {kept, (int64_t)heads * keep * 4}, {lengths_out, (int64_t)heads * 4}};
+    for (int i = 0; i < 6; ++i) {
+        for (const auto &x : in)
+            if (overlap(x.p, x.bytes, to[i].p, to[i].bytes)) return fail(AXR_EINVAL, "an output overlaps an input");
+        for (int j = 0; j < i; ++j)
+            if (overlap(to[j].p, to[j].bytes, to[i].p, to[i].bytes)) return fail(AXR_EINVAL, "two outputs overlap");
+    }
+    const EvictArgs a{idx, norms, V, vdtype, weights, lengths, capacity, keep, recent, heads, d, b,
+                      idx_out, norms_out, V_out, weights_out, capacity_out, kept, lengths_out};
+    const cudaError_t e = launch_evict(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(AXR_ECUDA, "eviction launch: %s", cudaGetErrorString(e));
     return ok();
 }
 

@@ -158,6 +158,38 @@ struct SignSelectArgs {
 };
 cudaError_t launch_sign_select(const SignSelectArgs &a, cudaStream_t stream);
 
+// Attention over packed prompts (prompt_attention.cu): prompt.cuh has the shape.
+struct PromptArgs;
+cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t stream);
+
+// Cache weights and eviction (cache_evict.cu).
+struct WeightArgs {
+    const float *scores;       // (heads*group, n)
+    float *weights;            // (heads, capacity), added to
+    const int32_t *lengths;    // (heads), or null: n keys each
+    int64_t n, capacity;
+    int heads, group;
+};
+cudaError_t launch_accumulate_weights(const WeightArgs &a, cudaStream_t stream);
+struct EvictArgs {
+    const uint8_t *idx;        // the cache: (heads, capacity) rows
+    const float *norms;
+    const void *V;
+    int vdtype;
+    const float *weights;
+    const int32_t *lengths;    // (heads)
+    int64_t capacity, keep, recent;
+    int heads, d, b;
+    uint8_t *idx_out;          // the cache that stays: (heads, capacity_out) rows
+    float *norms_out;
+    void *V_out;
+    float *weights_out;
+    int64_t capacity_out;
+    int32_t *kept;             // (heads, keep)
+    int32_t *lengths_out;      // (heads)
+};
+cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream);
+
 // Number of SMs of the current device (cached per device).
 int device_sm_count();
 

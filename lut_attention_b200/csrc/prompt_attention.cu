@@ -1,0 +1,151 @@
+// Attention over packed prompts on the CUDA cores (axr_prompt_attention for fp32
+// operands and the head widths without a tensor-core kernel): for query i of a
+// sequence with nq queries and nk keys,
+//     out_i = sum_{j <= i + nk - nq} softmax_j(q_i . k_j / sqrt(d)) V_j.
+// One CTA takes BM queries of one query head and walks its keys once
+// (cuda_core_attention.cuh); the grid holds a CTA for every tile the longest
+// packing could have, and a CTA finds its sequence by a warp's scan of cu_q.
+#include <type_traits>
+
+#include "axr_internal.cuh"
+#include "cuda_core_attention.cuh"
+#include "prompt.cuh"
+
+namespace axr {
+namespace {
+
+struct Params {
+    const void *q, *k, *v;
+    void *out;
+    float *lse;
+    PromptShape s;
+    float scale;               // log2(e) / sqrt(d)
+    AXR_DEBUG_ONLY(dbg::Span sp_q, sp_k, sp_v, sp_out, sp_lse, sp_cu_q, sp_cu_k;)
+};
+
+// eight consecutive elements as fp32
+template <typename T>
+__device__ __forceinline__ void load8(const T *src, float (&x)[8])
+{
+    if constexpr (sizeof(T) == 4) {
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(src)), b = __ldg(reinterpret_cast<const float4 *>(src) + 1);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    } else {
+        union { uint4 u; T t[8]; } a;
+        a.u = __ldg(reinterpret_cast<const uint4 *>(src));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = core::as_f32(a.t[i]);
+    }
+}
+
+template <int D, int BM, typename T>
+__global__ void __launch_bounds__(core::kThreads) prompt_kernel(const Params p)
+{
+    using S = core::Shape<D>;
+    extern __shared__ float4 smem4[];
+    core::Tile<D, BM> t(reinterpret_cast<float *>(smem4));
+    const int hq = blockIdx.y, h = hq / p.s.group;
+    PromptTile w;
+    if (!find_tile<BM>(p.s, blockIdx.x, w AXR_DEBUG_ONLY(, p.sp_cu_q, p.sp_cu_k))) return;
+
+    // rows of `rows` tokens from `row0` into padded shared rows, zeros past them
+    auto fill = [&](float *dst, int count, const void *base, int64_t head, int64_t stride, int hh, int row0, int rows,
+                    float scale AXR_DEBUG_ONLY(, const dbg::Span &sp)) {
+        for (int c = threadIdx.x; c < count * (D / 8); c += core::kThreads) {
+            const int r = c / (D / 8), e = c % (D / 8) * 8;
+            float x[8] = {};
+            const T *src = static_cast<const T *>(base) + hh * head + (row0 + r) * stride + e;
+            if (r < rows && AXR_IN(sp, src, 8 * sizeof(T))) load8<T>(src, x);
+            float4 *to = reinterpret_cast<float4 *>(dst + r * S::DS + e);
+            to[0] = make_float4(x[0] * scale, x[1] * scale, x[2] * scale, x[3] * scale);
+            to[1] = make_float4(x[4] * scale, x[5] * scale, x[6] * scale, x[7] * scale);
+        }
+    };
+    const int rows = min(BM, w.len_q - w.row);
+    fill(t.q, BM, p.q, p.s.q_head, p.s.q_row, hq, w.first_q + w.row, rows, p.scale AXR_DEBUG_ONLY(, p.sp_q));
+    t.reset();
+    const int past = w.len_k - w.len_q;                        // query i sees keys 0 .. i + past
+    const int keys = min(w.len_k, w.row + rows + past);        // that the tile's last query sees
+    for (int k0 = 0; k0 < keys; k0 += S::BN) {
+        __syncthreads();
+        fill(t.k, S::BN, p.k, p.s.k_head, p.s.k_row, h, w.first_k + k0, keys - k0, 1.0f AXR_DEBUG_ONLY(, p.sp_k));
+        fill(t.v, S::BN, p.v, p.s.v_head, p.s.v_row, h, w.first_k + k0, keys - k0, 1.0f AXR_DEBUG_ONLY(, p.sp_v));
+        __syncthreads();
+        t.step([&](int r) { return min(keys, w.row + r + past + 1) - k0; });
+    }
+#pragma unroll
+    for (int i = 0; i < t.R; ++i) {
+        const int r = t.row(i);
+        if (r >= rows) continue;
+        const int at = w.first_q + w.row + r;
+        const float inv = t.l[i] > 0.0f ? 1.0f / t.l[i] : t.l[i];      // 0 for no key, NaN stays NaN
+        T *dst = static_cast<T *>(p.out) + hq * p.s.o_head + at * p.s.o_row;
+#pragma unroll
+        for (int e = 0; e < t.E; ++e) {
+            T *to = dst + t.col(e);
+            if (AXR_IN(p.sp_out, to, sizeof(T))) *to = core::from_f32<T>(t.o[i][e] * inv);
+        }
+        if (p.lse && t.tx() == 0) {
+            float *to = p.lse + static_cast<int64_t>(hq) * p.s.total_q + at;
+            if (AXR_IN(p.sp_lse, to, 4)) *to = (t.m[i] + log2f(t.l[i])) * core::kLn2;
+        }
+    }
+}
+
+template <int D, typename T>
+cudaError_t launch_dt(const PromptArgs &a, cudaStream_t stream)
+{
+    // 64 queries for D <= 128; wider heads keep 32, whose output fits the registers
+    constexpr int BM = D <= 128 ? 64 : 32;
+    constexpr size_t kSmem = sizeof(float) * core::smem_floats<D, BM>();
+    static std::atomic<unsigned long long> done{0};
+    const auto kernel = prompt_kernel<D, BM, T>;
+    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), kSmem, done);
+    if (e != cudaSuccess) return e;
+    Params p{};
+    p.q = a.q;
+    p.k = a.K;
+    p.v = a.V;
+    p.out = a.out;
+    p.lse = a.lse;
+    p.s = a.s;
+    p.scale = core::kLog2e / sqrtf(static_cast<float>(D));
+    AXR_DEBUG_ONLY(const auto extent = [&](int64_t hd, int64_t st, int heads, int rows) {
+                       return rows == 0 ? 0 : ((heads - 1) * hd + (rows - 1) * st + D) * static_cast<int64_t>(sizeof(T));
+                   };
+                   const int hq = a.s.heads * a.s.group;
+                   p.sp_q = dbg::span(a.q, extent(a.s.q_head, a.s.q_row, hq, a.s.total_q));
+                   p.sp_k = dbg::span(a.K, extent(a.s.k_head, a.s.k_row, a.s.heads, a.s.total_k));
+                   p.sp_v = dbg::span(a.V, extent(a.s.v_head, a.s.v_row, a.s.heads, a.s.total_k));
+                   p.sp_out = dbg::span(a.out, extent(a.s.o_head, a.s.o_row, hq, a.s.total_q));
+                   p.sp_lse = dbg::span(a.lse, a.lse ? 4ull * hq * a.s.total_q : 0);
+                   p.sp_cu_q = dbg::span(a.s.cu_q, 4ull * (a.s.batch + 1));
+                   p.sp_cu_k = dbg::span(a.s.cu_k, 4ull * (a.s.batch + 1));)
+    kernel<<<dim3(prompt_tiles(a.s, BM), a.s.heads * a.s.group), core::kThreads, kSmem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const PromptArgs &a, cudaStream_t stream)
+{
+    switch (a.dtype) {
+    case AXR_F32: return launch_dt<D, float>(a, stream);
+    case AXR_F16: return launch_dt<D, __half>(a, stream);
+    default: return launch_dt<D, __nv_bfloat16>(a, stream);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t stream)
+{
+    switch (a.d) {
+    case 32: return launch_d<32>(a, stream);
+    case 64: return launch_d<64>(a, stream);
+    case 128: return launch_d<128>(a, stream);
+    case 256: return launch_d<256>(a, stream);
+    default: return launch_d<512>(a, stream);
+    }
+}
+
+}  // namespace axr

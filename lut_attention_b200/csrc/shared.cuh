@@ -1,0 +1,171 @@
+// Decode attention over a shared quantized prefix and each sequence's own
+// quantized keys: the split of the work that the kernels share.
+//
+// The work is a list of segments, each a block of queries against one run of
+// keys: per KV head (and block of BM of its batch * group queries) the prefix,
+// then per sequence and KV head its own keys against its `group` queries.  A
+// segment is cut into tiles of 128 keys; all tiles form one line, and CTA c of C
+// takes an equal stretch of it.  Where a CTA leaves a segment (or its stretch
+// ends) it writes the queries' running (o, m, l) to a slot of the workspace.
+// Along the line every step to another slot raises the segment or the CTA, so
+// segment + CTA numbers the slots without gaps in need of a table.  The last
+// kernel merges the slots of each query.  The split depends on the lengths
+// alone, so results repeat bit for bit.
+#pragma once
+
+#include <cstdint>
+
+#include "axr_internal.cuh"
+
+namespace axr {
+namespace shared {
+
+constexpr int kTileKeys = 128;
+
+// What every kernel of a call gets.
+struct Work {
+    const int32_t *lengths;            // (batch): own keys of each sequence, clamped to [0, capacity]
+    int n;                             // prefix keys
+    int capacity;
+    int batch, heads, group;
+    int d;
+    int bm;                            // queries of a prefix segment
+    int row_tiles;                     // ceil(batch * group / bm)
+    int slot_rows;                     // rows of a prefix slot: min(bm, batch * group)
+    int ctas;                          // CTAs of the main kernel (at most)
+    int min_tiles;                     // tiles a CTA gets at least
+    // workspace
+    void *rot;                         // rotated queries: batch * heads * group rows of d 32-bit words
+    float *rot_scale;                  // one factor per query (tensor-core kernel)
+    int32_t *own_start;                // (batch + 1): tiles of the own keys of sequences before b, per KV head
+    float *prefix_part;                // (heads * row_tiles + ctas) slots of slot_rows x (d + 2): o, m, l
+    float *own_part;                   // (batch * heads + ctas) slots of group x (d + 2)
+    AXR_DEBUG_ONLY(dbg::Span sp_lengths, sp_rot, sp_rot_scale, sp_own_start, sp_prefix_part, sp_own_part;)
+};
+
+struct Line {
+    int prefix_tiles;                  // per prefix segment
+    int64_t own_first;                 // first tile of the own segments
+    int64_t total;
+    int ctas;                          // that take part
+    __device__ int64_t begin(int c) const { return total * c / ctas; }
+    // the CTA that holds tile t
+    __device__ int owner(int64_t t) const { return static_cast<int>(((t + 1) * ctas - 1) / total); }
+};
+
+__device__ __forceinline__ int own_start(const Work &w, int b)
+{
+    return AXR_IN(w.sp_own_start, w.own_start + b, 4) ? w.own_start[b] : 0;
+}
+
+__device__ __forceinline__ Line line_of(const Work &w)
+{
+    Line x;
+    x.prefix_tiles = (w.n + kTileKeys - 1) / kTileKeys;
+    x.own_first = static_cast<int64_t>(w.heads) * w.row_tiles * x.prefix_tiles;
+    x.total = x.own_first + static_cast<int64_t>(w.heads) * own_start(w, w.batch);
+    const int64_t most = x.total / w.min_tiles;
+    x.ctas = static_cast<int>(most < 1 ? 1 : most < w.ctas ? most : w.ctas);
+    return x;
+}
+
+// A run of tiles of one segment.
+struct Run {
+    int head, seq;                     // KV head; sequence, or -1 for the prefix
+    int row0, rows;                    // prefix: queries row0 .. of the head's batch * group; own: 0, group
+    int tile, tiles;                   // tiles [tile, tile + tiles) of the segment
+    int keys;                          // keys of the segment
+    int64_t seg;                       // segment number among the prefix or own segments
+    int64_t base;                      // first key row (prefix: head * n, own: (seq * heads + head) * capacity)
+};
+
+// The run that starts at tile t and ends at the segment's end or at `end`.
+__device__ __forceinline__ Run run_at(const Work &w, const Line &x, int64_t t, int64_t end)
+{
+    Run r;
+    int64_t left;
+    if (t < x.own_first) {
+        r.seg = t / x.prefix_tiles;
+        r.tile = static_cast<int>(t - r.seg * x.prefix_tiles);
+        left = x.prefix_tiles - r.tile;
+        r.head = static_cast<int>(r.seg / w.row_tiles);
+        r.seq = -1;
+        r.row0 = static_cast<int>(r.seg % w.row_tiles) * w.bm;
+        r.rows = min(w.bm, w.batch * w.group - r.row0);
+        r.keys = w.n;
+        r.base = static_cast<int64_t>(r.head) * w.n;
+    } else {
+        const int64_t u = t - x.own_first;
+        int lo = 0, hi = w.batch;                             // the last b with heads * own_start[b] <= u
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (static_cast<int64_t>(w.heads) * own_start(w, mid) <= u) lo = mid;
+            else hi = mid;
+        }
+        const int s0 = own_start(w, lo), per = own_start(w, lo + 1) - s0;
+        const int64_t v = u - static_cast<int64_t>(w.heads) * s0;
+        r.head = static_cast<int>(v / per);
+        r.tile = static_cast<int>(v % per);
+        left = per - r.tile;
+        r.seq = lo;
+        r.row0 = 0;
+        r.rows = w.group;
+        const int len = AXR_IN(w.sp_lengths, w.lengths + lo, 4) ? w.lengths[lo] : 0;
+        r.keys = min(max(len, 0), w.capacity);
+        r.seg = static_cast<int64_t>(lo) * w.heads + r.head;
+        r.base = r.seg * w.capacity;
+    }
+    r.tiles = static_cast<int>(left < end - t ? left : end - t);
+    return r;
+}
+
+// the query row (of batch * heads * group) of row i of a run
+__device__ __forceinline__ int64_t query_row(const Work &w, const Run &r, int i)
+{
+    if (r.seq >= 0) return r.seg * w.group + i;
+    const int at = r.row0 + i;
+    return (static_cast<int64_t>(at / w.group) * w.heads + r.head) * w.group + at % w.group;
+}
+
+// where row i of a run writes its (o[d], m, l)
+__device__ __forceinline__ float *slot(const Work &w, const Run &r, int cta, int i)
+{
+    if (r.seq >= 0) return w.own_part + ((r.seg + cta) * w.group + i) * (w.d + 2);
+    return w.prefix_part + ((r.seg + cta) * w.slot_rows + i) * (w.d + 2);
+}
+
+// workspace of a call: fills the pointers of w from `base` and returns the bytes
+// (base may be null: bytes only).  All but base, n, lengths and capacity are set.
+int64_t lay_out(Work &w, void *base);
+
+}  // namespace shared
+
+struct SharedArgs {
+    const void *q;
+    int qdtype;
+    const uint8_t *prefix_idx;
+    const float *prefix_norms;
+    const void *prefix_V;
+    int64_t n;
+    const uint8_t *idx;
+    const float *norms;
+    const void *V;
+    int64_t capacity;
+    const int32_t *lengths;
+    int vdtype;
+    int batch, heads, group, d, b;
+    const int8_t *signs;
+    void *workspace;
+    void *out;                 // (batch*heads*group, d), vdtype
+    float *lse;                // (batch*heads*group), or null
+    Codebook cb;
+};
+
+// shared_attention.cu: the CUDA-core kernel, the kernel before (rotation, starts)
+// and the one after (merge) for both kernels
+cudaError_t launch_shared_before(const SharedArgs &a, const shared::Work &w, bool halves, cudaStream_t stream);
+cudaError_t launch_shared_after(const SharedArgs &a, const shared::Work &w, cudaStream_t stream);
+int64_t shared_workspace_bytes(int batch, int heads, int group, int d);
+cudaError_t launch_shared_attention(const SharedArgs &a, cudaStream_t stream);
+
+}  // namespace axr

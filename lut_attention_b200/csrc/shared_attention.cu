@@ -1,0 +1,505 @@
+// Decode attention of a batch whose sequences share a prefix (axr_attention_shared):
+// query head h*group + g of sequence s sees the prefix keys of KV head h and the
+// sequence's own keys,
+//     s_t = norm_t * sum_j q'_j c[idx_t[j]] / sqrt(d),   q' = H diag(signs) q / sqrt(d),
+//     out = sum_t softmax(s)_t V_t  over both.
+// The prefix is read once for all queries of a KV head.  Three kernels:
+//   before : rotates the queries (a warp per query) and sums the tile counts;
+//   main   : walks its stretch of tiles (shared.cuh); here on the CUDA cores in
+//            fp32, for fp32 values and the widths without a tensor-core kernel;
+//   after  : merges each query's slots, out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c.
+#include <type_traits>
+
+#include "axr_internal.cuh"
+#include "cuda_core_attention.cuh"
+#include "shared.cuh"
+
+namespace axr {
+namespace shared {
+
+int64_t lay_out(Work &w, void *base)
+{
+    int64_t at = 0;
+    const auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return base ? static_cast<void *>(static_cast<char *>(base) + here) : nullptr;
+    };
+    const int64_t rows = static_cast<int64_t>(w.batch) * w.heads * w.group;
+    const int64_t rot = rows * w.d * 4, scale = rows * 4, starts = (static_cast<int64_t>(w.batch) + 1) * 4;
+    const int64_t part = (static_cast<int64_t>(w.heads) * w.row_tiles + w.ctas) * w.slot_rows * (w.d + 2) * 4;
+    const int64_t own = (static_cast<int64_t>(w.batch) * w.heads + w.ctas) * w.group * (w.d + 2) * 4;
+    w.rot = take(rot);
+    w.rot_scale = static_cast<float *>(take(scale));
+    w.own_start = static_cast<int32_t *>(take(starts));
+    w.prefix_part = static_cast<float *>(take(part));
+    w.own_part = static_cast<float *>(take(own));
+    AXR_DEBUG_ONLY(w.sp_rot = dbg::span(w.rot, rot); w.sp_rot_scale = dbg::span(w.rot_scale, scale);
+                   w.sp_own_start = dbg::span(w.own_start, starts);
+                   w.sp_prefix_part = dbg::span(w.prefix_part, part); w.sp_own_part = dbg::span(w.own_part, own);
+                   w.sp_lengths = dbg::span(w.lengths, 4ull * w.batch);)
+    return at;
+}
+
+}  // namespace shared
+
+namespace {
+
+using shared::Line;
+using shared::Run;
+using shared::Work;
+
+constexpr int kBeforeWarps = 4;
+constexpr int kAfterWarps = 4;
+constexpr int kPrefixRows = 64;                // queries of a prefix segment on the CUDA cores
+constexpr int kOwnRows = 16;                   // rows of the tile that serves a sequence's own keys
+
+struct BeforeParams {
+    Work w;
+    const void *q;
+    int qdtype;
+    const int8_t *signs;
+    AXR_DEBUG_ONLY(dbg::Span sp_q, sp_signs;)
+};
+
+__device__ __forceinline__ float load_q(const void *q, int dtype, int64_t i)
+{
+    switch (dtype) {
+    case AXR_F32: return static_cast<const float *>(q)[i];
+    case AXR_F16: return __half2float(static_cast<const __half *>(q)[i]);
+    default: return __bfloat162float(static_cast<const __nv_bfloat16 *>(q)[i]);
+    }
+}
+
+// q'' = H diag(signs) q / d * log2(e): the rotation's and the temperature's
+// 1/sqrt(d), scores in units of log2.  Lane l holds coordinates l, l + 32, ...
+// kHalves: stored as fp16 pairs, d high parts then d low parts, of q'' times a
+// power of two that brings the row's largest coordinate into [1, 2); the
+// factor back goes to rot_scale.  Else fp32.
+template <int D, bool kHalves>
+__global__ void __launch_bounds__(kBeforeWarps * 32) before_kernel(const BeforeParams p)
+{
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    const int64_t rows = static_cast<int64_t>(p.w.batch) * p.w.heads * p.w.group;
+    if (blockIdx.x == 0) {                                    // tile counts of the own keys, summed over the batch
+        if (threadIdx.x >= 32) return;
+        int before = 0;
+        for (int b0 = 0; b0 < p.w.batch; b0 += 32) {
+            const int b = b0 + lane;
+            int len = 0;
+            if (b < p.w.batch && AXR_IN(p.w.sp_lengths, p.w.lengths + b, 4)) len = p.w.lengths[b];
+            len = min(max(len, 0), p.w.capacity);
+            const int tiles = (len + shared::kTileKeys - 1) / shared::kTileKeys;
+            int upto = tiles;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += x;
+            }
+            int *dst = p.w.own_start + b;
+            if (b < p.w.batch && AXR_IN(p.w.sp_own_start, dst, 4)) *dst = before + upto - tiles;
+            before += __shfl_sync(0xffffffffu, upto, 31);
+        }
+        int *dst = p.w.own_start + p.w.batch;
+        if (lane == 0 && AXR_IN(p.w.sp_own_start, dst, 4)) *dst = before;
+        return;
+    }
+    const int64_t row = static_cast<int64_t>(blockIdx.x - 1) * kBeforeWarps + (threadIdx.x >> 5);
+    if (row >= rows) return;
+    float x[E];
+    [[maybe_unused]] const int qb = dtype_bytes(p.qdtype);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int64_t at = row * D + e * 32 + lane;
+        const float v = AXR_IN(p.sp_q, static_cast<const char *>(p.q) + at * qb, qb) ? load_q(p.q, p.qdtype, at) : 0.0f;
+        const int8_t *sg = p.signs + e * 32 + lane;
+        x[e] = (AXR_IN(p.sp_signs, sg, 1) && *sg < 0) ? -v : v;
+    }
+#pragma unroll
+    for (int st = 1; st < 32; st <<= 1)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float o = __shfl_xor_sync(0xffffffffu, x[e], st);
+            x[e] = (lane & st) ? o - x[e] : x[e] + o;
+        }
+#pragma unroll
+    for (int st = 1; st < E; st <<= 1)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if ((e & st) == 0) {
+                const float a = x[e], b = x[e + st];
+                x[e] = a + b;
+                x[e + st] = a - b;
+            }
+    float top = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        x[e] *= core::kLog2e / D;
+        top = fmaxf(top, fabsf(x[e]));
+    }
+    if constexpr (!kHalves) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            float *dst = static_cast<float *>(p.w.rot) + row * D + e * 32 + lane;
+            if (AXR_IN(p.w.sp_rot, dst, 4)) *dst = x[e];
+        }
+    } else {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // exponents are kept where the factor and its inverse are both normal
+        int ex = top > 0.0f ? ilogbf(top) : 0;
+        ex = min(max(ex, -120), 120);
+        const float up = exp2f(static_cast<float>(-ex)), down = exp2f(static_cast<float>(ex));
+        __half *dst = static_cast<__half *>(p.w.rot) + row * 2 * D;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float v = x[e] * up;
+            const __half hi = __float2half_rn(v);
+            const __half lo = __float2half_rn(v - __half2float(hi));
+            __half *to = dst + e * 32 + lane;
+            if (AXR_IN(p.w.sp_rot, to, 2)) *to = hi;
+            if (AXR_IN(p.w.sp_rot, to + D, 2)) to[D] = lo;
+        }
+        if (lane == 0 && AXR_IN(p.w.sp_rot_scale, p.w.rot_scale + row, 4)) p.w.rot_scale[row] = down;
+    }
+}
+
+struct AfterParams {
+    Work w;
+    void *out;
+    float *lse;
+    AXR_DEBUG_ONLY(dbg::Span sp_out, sp_lse;)
+};
+
+// one CTA per query: its warps take every kAfterWarps-th slot and meet in shared memory
+template <int D, typename T>
+__global__ void __launch_bounds__(kAfterWarps * 32) after_kernel(const AfterParams p)
+{
+    constexpr int E = D / 32;
+    __shared__ float s_o[kAfterWarps][D], s_m[kAfterWarps], s_l[kAfterWarps];
+    const Work &w = p.w;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = blockIdx.x;
+    const int g = static_cast<int>(row % w.group);
+    const int64_t sh = row / w.group;                         // sequence * heads + head
+    const int h = static_cast<int>(sh % w.heads), b = static_cast<int>(sh / w.heads);
+    const Line x = shared::line_of(w);
+
+    float m = -INFINITY, l = 0.0f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+    // one slot's (o, m, l) into this warp's sums
+    auto add = [&](const float *src AXR_DEBUG_ONLY(, const dbg::Span &sp)) {
+        if (!AXR_IN(sp, src, (D + 2) * 4)) return;
+        const float sm = src[D], sl = src[D + 1];
+        float v[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = src[e * 32 + lane];
+        const float top = fmaxf(m, sm);
+        const float base = top == -INFINITY ? 0.0f : top;
+        const float a = exp2f(m - base), c = exp2f(sm - base);
+        l = fmaf(l, a, sl * c);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], a, v[e] * c);
+        m = top;
+    };
+    if (x.prefix_tiles > 0) {
+        const int at = b * w.group + g;
+        const int64_t seg = static_cast<int64_t>(h) * w.row_tiles + at / w.bm;
+        const int c0 = x.owner(seg * x.prefix_tiles), c1 = x.owner((seg + 1) * x.prefix_tiles - 1);
+        for (int c = c0 + warp; c <= c1; c += kAfterWarps)
+            add(w.prefix_part + ((seg + c) * w.slot_rows + at % w.bm) * (D + 2) AXR_DEBUG_ONLY(, w.sp_prefix_part));
+    }
+    const int s0 = shared::own_start(w, b), per = shared::own_start(w, b + 1) - s0;
+    if (per > 0) {
+        const int64_t t0 = x.own_first + static_cast<int64_t>(w.heads) * s0 + static_cast<int64_t>(h) * per;
+        const int c0 = x.owner(t0), c1 = x.owner(t0 + per - 1);
+        for (int c = c0 + warp; c <= c1; c += kAfterWarps)
+            add(w.own_part + ((sh + c) * w.group + g) * (D + 2) AXR_DEBUG_ONLY(, w.sp_own_part));
+    }
+    if (lane == 0) {
+        s_m[warp] = m;
+        s_l[warp] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_o[warp][e * 32 + lane] = o[e];
+    __syncthreads();
+    float top = -INFINITY, sum = 0.0f, f[kAfterWarps];
+#pragma unroll
+    for (int i = 0; i < kAfterWarps; ++i) top = fmaxf(top, s_m[i]);
+    const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+    for (int i = 0; i < kAfterWarps; ++i) {
+        f[i] = exp2f(s_m[i] - base);
+        sum = fmaf(s_l[i], f[i], sum);
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : sum;          // 0 without a key, NaN stays NaN
+    for (int j = threadIdx.x; j < D; j += kAfterWarps * 32) {
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kAfterWarps; ++i) v = fmaf(s_o[i][j], f[i], v);
+        T *dst = static_cast<T *>(p.out) + row * D + j;
+        if (AXR_IN(p.sp_out, dst, sizeof(T))) *dst = core::from_f32<T>(v * inv);
+    }
+    if (p.lse && threadIdx.x == 0 && AXR_IN(p.sp_lse, p.lse + row, 4)) p.lse[row] = (top + log2f(sum)) * core::kLn2;
+}
+
+struct MainParams {
+    Work w;
+    const uint8_t *prefix_idx, *idx;
+    const float *prefix_norms, *norms;
+    const void *prefix_V, *V;
+    float cent[kMaxLevels];
+    AXR_DEBUG_ONLY(dbg::Span sp_prefix_idx, sp_idx, sp_prefix_norms, sp_norms, sp_prefix_V, sp_V;)
+};
+
+// a run of tiles with a tile of BM queries
+template <int D, int B, int BM, typename T>
+__device__ void take_run(const MainParams &p, const Run &r, float *smem, const float *cent)
+{
+    using S = core::Shape<D>;
+    constexpr int P = D * B / 8;
+    core::Tile<D, BM> t(smem);
+    const Work &w = p.w;
+    const bool own = r.seq >= 0;
+    const uint8_t *idx = (own ? p.idx : p.prefix_idx) + r.base * P;
+    const float *norms = (own ? p.norms : p.prefix_norms) + r.base;
+    const T *V = static_cast<const T *>(own ? p.V : p.prefix_V) + r.base * D;
+    AXR_DEBUG_ONLY(const dbg::Span sp_i = own ? p.sp_idx : p.sp_prefix_idx;
+                   const dbg::Span sp_n = own ? p.sp_norms : p.sp_prefix_norms;
+                   const dbg::Span sp_v = own ? p.sp_V : p.sp_prefix_V;)
+    __syncthreads();                                          // the last run's readers are done
+    for (int c = threadIdx.x; c < BM * (D / 4); c += core::kThreads) {
+        const int i = c / (D / 4), e = c % (D / 4) * 4;
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (i < r.rows) {
+            const float *src = static_cast<const float *>(w.rot) + shared::query_row(w, r, i) * D + e;
+            if (AXR_IN(w.sp_rot, src, 16)) x = *reinterpret_cast<const float4 *>(src);
+        }
+        *reinterpret_cast<float4 *>(t.q + i * S::DS + e) = x;
+    }
+    t.reset();
+    const int first = r.tile * shared::kTileKeys;
+    const int last = min(r.keys, (r.tile + r.tiles) * shared::kTileKeys);
+    for (int k0 = first; k0 < last; k0 += S::BN) {
+        __syncthreads();
+        const int keys = min(S::BN, last - k0);
+        for (int c = threadIdx.x; c < S::BN * (D / 8); c += core::kThreads) {
+            const int i = c / (D / 8), e = c % (D / 8) * 8;
+            float kx[8] = {}, vx[8] = {};
+            if (i < keys) {
+                // eight codes sit in B bytes
+                const uint8_t *src = idx + static_cast<int64_t>(k0 + i) * P + e / 8 * B;
+                uint32_t word = 0;
+                if (AXR_IN(sp_i, src, B)) {
+#pragma unroll
+                    for (int y = 0; y < B; ++y) word |= static_cast<uint32_t>(__ldg(src + y)) << (8 * y);
+                }
+                const float nk = AXR_IN(sp_n, norms + k0 + i, 4) ? __ldg(norms + k0 + i) : 0.0f;
+#pragma unroll
+                for (int y = 0; y < 8; ++y) kx[y] = nk * cent[(word >> (B * y)) & ((1 << B) - 1)];
+                const T *vs = V + static_cast<int64_t>(k0 + i) * D + e;
+                if (AXR_IN(sp_v, vs, 8 * sizeof(T))) {
+                    union { uint4 u[sizeof(T) / 2]; T x[8]; } a;
+#pragma unroll
+                    for (int y = 0; y < static_cast<int>(sizeof(T)) / 2; ++y) a.u[y] = __ldg(reinterpret_cast<const uint4 *>(vs) + y);
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) vx[y] = core::as_f32(a.x[y]);
+                }
+            }
+            float4 *tk = reinterpret_cast<float4 *>(t.k + i * S::DS + e), *tv = reinterpret_cast<float4 *>(t.v + i * S::DS + e);
+            tk[0] = make_float4(kx[0], kx[1], kx[2], kx[3]);
+            tk[1] = make_float4(kx[4], kx[5], kx[6], kx[7]);
+            tv[0] = make_float4(vx[0], vx[1], vx[2], vx[3]);
+            tv[1] = make_float4(vx[4], vx[5], vx[6], vx[7]);
+        }
+        __syncthreads();
+        t.step([&](int) { return keys; });
+    }
+#pragma unroll
+    for (int i = 0; i < t.R; ++i) {
+        if (t.row(i) >= r.rows) continue;
+        float *dst = shared::slot(w, r, blockIdx.x, t.row(i));
+        if (!AXR_IN((own ? w.sp_own_part : w.sp_prefix_part), dst, (D + 2) * 4)) continue;
+#pragma unroll
+        for (int e = 0; e < t.E; ++e) dst[t.col(e)] = t.o[i][e];
+        if (t.tx() == 0) {
+            dst[D] = t.m[i];
+            dst[D + 1] = t.l[i];
+        }
+    }
+}
+
+template <int D, int B, typename T>
+__global__ void __launch_bounds__(core::kThreads) main_kernel(const MainParams p)
+{
+    extern __shared__ float4 smem4[];
+    __shared__ float cent[kMaxLevels];
+    if (threadIdx.x < (1 << B)) cent[threadIdx.x] = p.cent[threadIdx.x];
+    const Line x = shared::line_of(p.w);
+    if (blockIdx.x >= x.ctas) return;
+    float *smem = reinterpret_cast<float *>(smem4);
+    const int64_t end = x.begin(blockIdx.x + 1);
+    for (int64_t t = x.begin(blockIdx.x); t < end;) {
+        const Run r = shared::run_at(p.w, x, t, end);
+        if (r.seq >= 0) take_run<D, B, kOwnRows, T>(p, r, smem, cent);
+        else take_run<D, B, D <= 128 ? kPrefixRows : 32, T>(p, r, smem, cent);
+        t += r.tiles;
+    }
+}
+
+template <int D>
+constexpr int prefix_rows() { return D <= 128 ? kPrefixRows : 32; }
+
+template <int D, int B, typename T>
+cudaError_t launch_main(const SharedArgs &a, const Work &w, cudaStream_t stream)
+{
+    constexpr size_t kSmem = sizeof(float) * core::smem_floats<D, prefix_rows<D>()>();
+    static std::atomic<unsigned long long> done{0};
+    const auto kernel = main_kernel<D, B, T>;
+    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), kSmem, done);
+    if (e != cudaSuccess) return e;
+    MainParams p{};
+    p.w = w;
+    p.prefix_idx = a.prefix_idx;
+    p.idx = a.idx;
+    p.prefix_norms = a.prefix_norms;
+    p.norms = a.norms;
+    p.prefix_V = a.prefix_V;
+    p.V = a.V;
+    for (int i = 0; i < (1 << B); ++i) p.cent[i] = a.cb.centroids[i];
+    AXR_DEBUG_ONLY(const uint64_t rows = static_cast<uint64_t>(a.heads) * a.n;
+                   const uint64_t own = static_cast<uint64_t>(a.batch) * a.heads * a.capacity;
+                   p.sp_prefix_idx = dbg::span(a.prefix_idx, rows * (D * B / 8));
+                   p.sp_prefix_norms = dbg::span(a.prefix_norms, rows * 4);
+                   p.sp_prefix_V = dbg::span(a.prefix_V, rows * D * sizeof(T));
+                   p.sp_idx = dbg::span(a.idx, own * (D * B / 8));
+                   p.sp_norms = dbg::span(a.norms, own * 4);
+                   p.sp_V = dbg::span(a.V, own * D * sizeof(T));)
+    kernel<<<w.ctas, core::kThreads, kSmem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <int D, typename T>
+cudaError_t launch_main_b(const SharedArgs &a, const Work &w, cudaStream_t stream)
+{
+    switch (a.b) {
+    case 1: return launch_main<D, 1, T>(a, w, stream);
+    case 2: return launch_main<D, 2, T>(a, w, stream);
+    case 3: return launch_main<D, 3, T>(a, w, stream);
+    default: return launch_main<D, 4, T>(a, w, stream);
+    }
+}
+
+template <int D>
+cudaError_t launch_main_d(const SharedArgs &a, const Work &w, cudaStream_t stream)
+{
+    switch (a.vdtype) {
+    case AXR_F32: return launch_main_b<D, float>(a, w, stream);
+    case AXR_F16: return launch_main_b<D, __half>(a, w, stream);
+    default: return launch_main_b<D, __nv_bfloat16>(a, w, stream);
+    }
+}
+
+Work work_of(int batch, int heads, int group, int d)
+{
+    Work w{};
+    w.batch = batch;
+    w.heads = heads;
+    w.group = group;
+    w.d = d;
+    w.bm = d <= 128 ? kPrefixRows : 32;
+    const int rows = batch * group;
+    w.row_tiles = (rows + w.bm - 1) / w.bm;
+    w.slot_rows = rows < w.bm ? rows : w.bm;
+    w.ctas = device_sm_count() * (d <= 128 ? 2 : 1);          // as many as are resident
+    w.min_tiles = 1;
+    return w;
+}
+
+template <int D>
+cudaError_t launch_before_d(const SharedArgs &a, const Work &w, bool halves, cudaStream_t stream)
+{
+    BeforeParams p{};
+    p.w = w;
+    p.q = a.q;
+    p.qdtype = a.qdtype;
+    p.signs = a.signs;
+    const int64_t rows = static_cast<int64_t>(w.batch) * w.heads * w.group;
+    AXR_DEBUG_ONLY(p.sp_q = dbg::span(a.q, rows * D * dtype_bytes(a.qdtype)); p.sp_signs = dbg::span(a.signs, D);)
+    const int grid = 1 + static_cast<int>((rows + kBeforeWarps - 1) / kBeforeWarps);
+    if (halves) before_kernel<D, true><<<grid, kBeforeWarps * 32, 0, stream>>>(p);
+    else before_kernel<D, false><<<grid, kBeforeWarps * 32, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_after_d(const SharedArgs &a, const Work &w, cudaStream_t stream)
+{
+    AfterParams p{};
+    p.w = w;
+    p.out = a.out;
+    p.lse = a.lse;
+    const int rows = w.batch * w.heads * w.group;
+    AXR_DEBUG_ONLY(p.sp_out = dbg::span(a.out, static_cast<uint64_t>(rows) * D * dtype_bytes(a.vdtype));
+                   p.sp_lse = dbg::span(a.lse, a.lse ? 4ull * rows : 0);)
+    switch (a.vdtype) {
+    case AXR_F32: after_kernel<D, float><<<rows, kAfterWarps * 32, 0, stream>>>(p); break;
+    case AXR_F16: after_kernel<D, __half><<<rows, kAfterWarps * 32, 0, stream>>>(p); break;
+    default: after_kernel<D, __nv_bfloat16><<<rows, kAfterWarps * 32, 0, stream>>>(p); break;
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_shared_before(const SharedArgs &a, const Work &w, bool halves, cudaStream_t stream)
+{
+    switch (a.d) {
+    case 32: return launch_before_d<32>(a, w, halves, stream);
+    case 64: return launch_before_d<64>(a, w, halves, stream);
+    case 128: return launch_before_d<128>(a, w, halves, stream);
+    case 256: return launch_before_d<256>(a, w, halves, stream);
+    default: return launch_before_d<512>(a, w, halves, stream);
+    }
+}
+
+cudaError_t launch_shared_after(const SharedArgs &a, const Work &w, cudaStream_t stream)
+{
+    switch (a.d) {
+    case 32: return launch_after_d<32>(a, w, stream);
+    case 64: return launch_after_d<64>(a, w, stream);
+    case 128: return launch_after_d<128>(a, w, stream);
+    case 256: return launch_after_d<256>(a, w, stream);
+    default: return launch_after_d<512>(a, w, stream);
+    }
+}
+
+int64_t shared_workspace_bytes(int batch, int heads, int group, int d)
+{
+    Work w = work_of(batch, heads, group, d);
+    return shared::lay_out(w, nullptr);
+}
+
+cudaError_t launch_shared_attention(const SharedArgs &a, cudaStream_t stream)
+{
+    Work w = work_of(a.batch, a.heads, a.group, a.d);
+    w.n = static_cast<int>(a.n);
+    w.capacity = static_cast<int>(a.capacity);
+    w.lengths = a.lengths;
+    shared::lay_out(w, a.workspace);
+    cudaError_t e = launch_shared_before(a, w, false, stream);
+    if (e != cudaSuccess) return e;
+    switch (a.d) {
+    case 32: e = launch_main_d<32>(a, w, stream); break;
+    case 64: e = launch_main_d<64>(a, w, stream); break;
+    case 128: e = launch_main_d<128>(a, w, stream); break;
+    case 256: e = launch_main_d<256>(a, w, stream); break;
+    default: e = launch_main_d<512>(a, w, stream); break;
+    }
+    if (e != cudaSuccess) return e;
+    return launch_shared_after(a, w, stream);
+}
+
+}  // namespace axr
