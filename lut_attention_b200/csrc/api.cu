@@ -524,7 +524,8 @@ extern "C" int axr_prompt_attention(const void *q, const void *K, const void *V,
     a.lse = lse;
     a.s = PromptShape{cu_q, cu_k, batch, heads, group, (int)total_q, (int)total_k, strides[0], strides[1],
                       strides[2], strides[3], strides[4], strides[5], strides[6], strides[7]};
-    const cudaError_t e = launch_prompt_attention(a, reinterpret_cast<cudaStream_t>(stream));
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = prompt_tc_supported(a) ? launch_prompt_attention_tc(a, st) : launch_prompt_attention(a, st);
     if (e != cudaSuccess) return fail(AXR_ECUDA, "prompt attention launch: %s", cudaGetErrorString(e));
     return ok();
 }
@@ -674,9 +675,10 @@ extern "C" int axr_device_status(int clear, unsigned int *status)
     if (e != cudaSuccess) return fail(AXR_ECUDA, "device synchronize: %s", cudaGetErrorString(e));
     const unsigned int q = quantize_tc_status(clear != 0);
     const unsigned int r = scores_tc_status(clear != 0);
+    const unsigned int t = prompt_tc_status(clear != 0);
     const unsigned int bnd = dbg::read_all(clear != 0);
-    if (q == ~0u || r == ~0u || bnd == ~0u) return fail(AXR_ECUDA, "reading the device status words failed");
-    *status = q | r | bnd;
+    if (q == ~0u || r == ~0u || t == ~0u || bnd == ~0u) return fail(AXR_ECUDA, "reading the device status words failed");
+    *status = q | r | t | bnd;
     return ok();
 }
 

@@ -161,6 +161,10 @@ cudaError_t launch_sign_select(const SignSelectArgs &a, cudaStream_t stream);
 // Attention over packed prompts (prompt_attention.cu): prompt.cuh has the shape.
 struct PromptArgs;
 cudaError_t launch_prompt_attention(const PromptArgs &a, cudaStream_t stream);
+// Tensor-core form (prompt_attention_tc.cu): 16-bit types, d = 64, 128, 256.
+bool prompt_tc_supported(const PromptArgs &a);
+cudaError_t launch_prompt_attention_tc(const PromptArgs &a, cudaStream_t stream);
+unsigned int prompt_tc_status(bool clear);
 
 // Cache weights and eviction (cache_evict.cu).
 struct WeightArgs {

@@ -1,0 +1,675 @@
+// Attention over packed prompts on the 5th-generation tensor cores
+// (axr_prompt_attention for 16-bit types, d = 64, 128, 256).  For a tile of 128
+// queries and successive tiles of 128 keys, one pass with the running maximum m
+// and sum l of each query's softmax:
+//     S = Q K^T                     (fp32 in tensor memory)
+//     p = 2^((S - m) log2(e)/sqrt(d))   (one thread per query, fp32, rounded to the type)
+//     O += P V,  l += sum p         (O in tensor memory)
+// P overwrites S in tensor memory and is the products' A operand from there, so
+// neither S nor P touches shared memory.  m is raised, and O and l rescaled, only
+// when a tile's maximum exceeds it by more than 2^8: until then the weights are
+// merely larger than 1, which fp32 sums and 16-bit weights hold as well.  That
+// makes the rescale rare enough for the softmax warps to do it themselves.
+//
+// A persistent CTA per SM with one TMA warp, one MMA warp and a softmax
+// warpgroup per query tile in flight:
+//   d <= 128: two query tiles (256 queries).  Their S take turns: while the tensor
+//     cores run one tile's products, the other tile's warps are in their softmax.
+//   d = 256: one query tile (O takes half of tensor memory) with two S buffers;
+//     the products of the next tile of keys run under the softmax of this one.
+// K and V pass through a ring of 32 KB (d = 64: 16 KB) pieces: a tile of K or V, at
+// d = 256 half of one (128 dimensions of K, 64 keys of V).
+//
+// Work items are (tile of queries, query head), dealt round-robin with the tiles
+// that see most keys first.  The next item's loads and first products run under
+// the epilogue of this one.
+//
+// Every wait is bounded (sm100.cuh); a wait that runs out records a status bit
+// and ends its role.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "axr_internal.cuh"
+#include "prompt.cuh"
+#include "sm100.cuh"
+
+namespace axr {
+namespace {
+
+using namespace sm100;
+
+constexpr int kTile = 128;                     // queries of a tile, keys of a tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLazy = 8.0f;                  // log2 of the growth that rescales
+constexpr int kMaxStages = 12;
+
+__device__ unsigned int g_status;
+
+template <int D>
+struct Cfg {
+    static constexpr int NQ = D <= 128 ? 2 : 1;                // query tiles in flight
+    static constexpr int BM = kTile * NQ;                      // queries of an item
+    static constexpr int QBlocks = D / 64;                     // 64-element blocks of a row
+    static constexpr int QBytes = kTile * D * 2;               // one query tile
+    static constexpr int Pieces = D <= 128 ? 1 : D / 128;      // ring pieces of a K or V tile
+    static constexpr int PieceBytes = kTile * D * 2 / Pieces;
+    static constexpr int VKeys = kTile / Pieces;               // keys of a V piece
+    static constexpr int Stages = D == 64 ? 11 : 5;
+    static constexpr int SoftmaxWarps = 4 * NQ;
+    static constexpr int WarpMma = SoftmaxWarps, WarpTma = SoftmaxWarps + 1;
+    // two query tiles: a third warpgroup (TMA, MMA, two idle warps) hands registers
+    // to the softmax warps, of the 168 a thread that 384 threads get at launch
+    static constexpr int Threads = NQ == 2 ? 384 : 192;
+    static constexpr int SoftmaxRegs = 224, OtherRegs = 56;
+    static_assert(2 * SoftmaxRegs + OtherRegs <= 3 * 168, "registers of the block");
+    static constexpr int OCol = 2 * kTile;                     // S buffers first, then O
+    static_assert(OCol + NQ * D <= 512, "tensor memory");
+    static_assert(Stages <= kMaxStages, "ring");
+};
+
+struct Book {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[2];        // S of a buffer is complete
+    uint64_t p_full[2];        // its P is written (and O rescaled where needed)
+    uint64_t o_done[2];        // a query tile's latest P V is complete
+    uint64_t drain;
+    uint32_t tmem_base;
+};
+
+template <int D>
+constexpr size_t smem_bytes() { return 1024 + Cfg<D>::NQ * Cfg<D>::QBytes + Cfg<D>::Stages * Cfg<D>::PieceBytes + sizeof(Book); }
+static_assert(smem_bytes<64>() <= 232448 && smem_bytes<128>() <= 232448 && smem_bytes<256>() <= 232448, "shared memory");
+
+struct Params {
+    CUtensorMap q, k, v;       // (heads, rows, d), box 64 x 128 rows (v at d = 256: 64 rows)
+    PromptShape s;
+    void *out;
+    float *lse;
+    float scale;               // log2(e) / sqrt(d)
+    int tiles;                 // items per query head (at most)
+    AXR_DEBUG_ONLY(dbg::Span sp_out, sp_lse, sp_cu_q, sp_cu_k;)
+};
+
+// What an item's roles need to know.
+struct Item {
+    PromptTile t;
+    int hq;
+    int rows[2];               // queries of each query tile
+    int n[2];                  // tiles of keys each of them sees
+    int most;                  // tiles of keys loaded
+};
+
+template <int D>
+__device__ __forceinline__ bool item_at(const Params &p, int64_t i, Item &x)
+{
+    using C = Cfg<D>;
+    const int hqs = p.s.heads * p.s.group;
+    x.hq = static_cast<int>(i % hqs);
+    if (!find_tile<C::BM>(p.s, static_cast<int>(i / hqs), x.t AXR_DEBUG_ONLY(, p.sp_cu_q, p.sp_cu_k))) return false;
+    x.most = 0;
+#pragma unroll
+    for (int t = 0; t < C::NQ; ++t) {
+        const int first = x.t.row + t * kTile;
+        x.rows[t] = min(max(x.t.len_q - first, 0), kTile);
+        const int keys = x.rows[t] > 0 ? max(first + x.rows[t] + x.t.len_k - x.t.len_q, 0) : 0;
+        x.n[t] = (keys + kTile - 1) / kTile;
+        x.most = max(x.most, x.n[t]);
+    }
+    return true;
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// two weights as packed 16-bit values, the first in the low half
+template <bool kBF16>
+__device__ __forceinline__ uint32_t pack16(float a, float b)
+{
+    uint32_t r;
+    if constexpr (kBF16) asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(a), "f"(b));
+    else asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// fp16 weights carry a factor 2^7: with the lazy maximum they reach 2^15 at most,
+// and those as small as 2^-21 of the largest are still normal numbers
+template <bool kBF16>
+constexpr float kBias = kBF16 ? 0.0f : 7.0f;
+
+// Softmax of 64 scores: p = 2^(s * scale + c), their sum into (sum0, sum1), packed into w
+template <bool kBF16>
+__device__ __forceinline__ void weights64(const uint32_t (&s)[64], uint64_t scale2, uint64_t c2, uint64_t &sum0,
+                                          uint64_t &sum1, uint32_t (&w)[32])
+{
+#pragma unroll
+    for (int i = 0; i < 64; i += 4) {
+        float a, b, c, d;
+        unpair(fma2(pair(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), scale2, c2), a, b);
+        unpair(fma2(pair(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), scale2, c2), c, d);
+        a = ex2(a);
+        b = ex2(b);
+        c = ex2(c);
+        d = ex2(d);
+        sum0 = add2(sum0, pair(a, b));
+        sum1 = add2(sum1, pair(c, d));
+        w[i / 2] = pack16<kBF16>(a, b);
+        w[i / 2 + 1] = pack16<kBF16>(c, d);
+    }
+}
+
+// The softmax warpgroup of query tile t (buffer t; at NQ = 1 buffers 0 and 1 in
+// turn).  Thread = query.
+template <int D, bool kBF16>
+__device__ void softmax_role(const Params &p, Book &B, int t, uint32_t tmem)
+{
+    using C = Cfg<D>;
+    const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t o_at = tmem + lanes + C::OCol + t * D;
+    const int64_t items = static_cast<int64_t>(p.tiles) * p.s.heads * p.s.group;
+    uint32_t s_count[2] = {0, 0}, o_count = 0;                 // phases of s_full and o_done seen
+    for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+        Item x;
+        if (!item_at<D>(p, i, x)) break;
+        const int rows = x.rows[t], n = x.n[t];
+        const bool idle = warp * 32 >= rows;                   // no query of this warp
+        const int first = x.t.row + t * kTile + warp * 32;     // the warp's first query
+        const int past = x.t.len_k - x.t.len_q;
+        float m = -INFINITY, l = 0.0f;
+        for (int j = 0; j < n; ++j) {
+            const int buf = C::NQ == 2 ? t : j & 1;
+            if (!mbar_wait_warp(smem_u32(&B.s_full[buf]), s_count[buf] & 1)) {
+                if (lane == 0) atomicOr(&g_status, kErrTimeoutMma);
+                return;
+            }
+            ++s_count[buf];
+            if (!idle) {
+                tc_fence_after_sync();
+                const uint32_t s_at = tmem + lanes + buf * kTile;
+                uint32_t a[64], b[64];
+                tmem_ld64(s_at, a);
+                tmem_ld64(s_at + 64, b);
+                const int seen = first + past + 1 - j * kTile; // keys of the tile that the warp's first query sees
+                if (seen < kTile) {
+                    const int lim = seen + lane;
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) {
+                        if (c >= lim) a[c] = 0xff800000u;
+                        if (c + 64 >= lim) b[c] = 0xff800000u;
+                    }
+                }
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < 64; c += 4)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        top[e] = fmaxf(top[e], fmaxf(__uint_as_float(a[c + e]), __uint_as_float(b[c + e])));
+                const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                if (j == 0) {
+                    m = mx;
+                } else if (__any_sync(0xffffffffu, (mx - m) * p.scale > kLazy)) {
+                    // the last P V must be complete before O is rescaled
+                    if (!mbar_wait_warp(smem_u32(&B.o_done[t]), (o_count + j - 1) & 1)) {
+                        if (lane == 0) atomicOr(&g_status, kErrTimeoutMma);
+                        return;
+                    }
+                    tc_fence_after_sync();
+                    const float up = fmaxf(m, mx);
+                    const float f = m == -INFINITY ? 0.0f : ex2((m - up) * p.scale);
+                    m = up;
+                    l *= f;
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o_at + c, o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st32(o_at + c, o);
+                    }
+                }
+                // a query that has seen no key keeps weights of 0
+                const float c0 = m == -INFINITY ? 0.0f : kBias<kBF16> - m * p.scale;
+                const uint64_t scale2 = pair(p.scale, p.scale), c2 = pair(c0, c0);
+                uint64_t sum0 = pair(l, 0.0f), sum1 = pair(0.0f, 0.0f);
+                uint32_t w[32];
+                weights64<kBF16>(a, scale2, c2, sum0, sum1, w);
+                tmem_st32(s_at, w);
+                weights64<kBF16>(b, scale2, c2, sum0, sum1, w);
+                tmem_st32(s_at + 32, w);
+                float s0, s1, s2, s3;
+                unpair(sum0, s0, s1);
+                unpair(sum1, s2, s3);
+                l = (s0 + s1) + (s2 + s3);
+                tmem_wait_st();
+                tc_fence_before_sync();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&B.p_full[buf]));
+        }
+        o_count += n;
+        // the last two P V in turn: with two S buffers both may still be running, and a
+        // wait tells a phase only from its neighbours
+        for (int k = n < 2 ? n : 2; k > 0; --k)
+            if (!mbar_wait_warp(smem_u32(&B.o_done[t]), (o_count - k) & 1)) {
+                if (lane == 0) atomicOr(&g_status, kErrTimeoutMma);
+                return;
+            }
+        if (idle) continue;
+        tc_fence_after_sync();
+        const int r = warp * 32 + lane;
+        const int64_t at = x.t.first_q + x.t.row + t * kTile + r;
+        const float inv = l > 0.0f ? 1.0f / l : l;             // 0 for no key, NaN stays NaN
+        char *dst = static_cast<char *>(p.out) + (x.hq * p.s.o_head + at * p.s.o_row) * 2;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            if (n > 0) {
+                tmem_ld32(o_at + c, o);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = 0u;
+            }
+            if (r < rows) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    uint4 v;
+                    v.x = pack16<kBF16>(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                    v.y = pack16<kBF16>(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                    v.z = pack16<kBF16>(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                    v.w = pack16<kBF16>(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                    uint4 *to = reinterpret_cast<uint4 *>(dst + (c + e) * 2);
+                    if (AXR_IN(p.sp_out, to, 16)) *to = v;
+                }
+            }
+        }
+        if (p.lse && r < rows) {
+            float *to = p.lse + static_cast<int64_t>(x.hq) * p.s.total_q + at;
+            const float base = m == -INFINITY ? -INFINITY : m * p.scale - kBias<kBF16>;
+            if (AXR_IN(p.sp_lse, to, 4)) *to = (base + log2f(l)) * kLn2;
+        }
+        tc_fence_before_sync();                                // O is read before the next item's P is announced
+    }
+}
+
+template <int D>
+__device__ void tma_role(const Params &p, Book &B, uint32_t q_smem, uint32_t ring)
+{
+    using C = Cfg<D>;
+    const int lane = threadIdx.x & 31;
+    const int64_t items = static_cast<int64_t>(p.tiles) * p.s.heads * p.s.group;
+    uint32_t pieces = 0, q_count[2] = {0, 0};
+    bool ok = true;
+    // the next stage of the ring, free; its barrier expects a piece
+    auto next = [&](uint32_t &dst, uint32_t &bar) {
+        const int s = pieces % C::Stages;
+        if (!mbar_wait(smem_u32(&B.empty[s]), ((pieces / C::Stages) & 1) ^ 1)) {
+            atomicOr(&g_status, kErrTimeoutMma);
+            return false;
+        }
+        ++pieces;
+        dst = ring + s * C::PieceBytes;
+        bar = smem_u32(&B.full[s]);
+        mbar_arrive_expect_tx(bar, C::PieceBytes);
+        return true;
+    };
+    for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+        Item x;
+        if (!item_at<D>(p, i, x)) break;
+        if (lane == 0 && ok) {
+            const int h = x.hq / p.s.group;
+            auto load_q = [&](int t) {
+                if (x.n[t] == 0) return true;
+                if (!mbar_wait(smem_u32(&B.q_empty[t]), (q_count[t] & 1) ^ 1)) {
+                    atomicOr(&g_status, kErrTimeoutMma);
+                    return false;
+                }
+                ++q_count[t];
+                const uint32_t bar = smem_u32(&B.q_full[t]);
+                mbar_arrive_expect_tx(bar, C::QBytes);
+                for (int c = 0; c < C::QBlocks; ++c)
+                    tma_load_3d(q_smem + t * C::QBytes + c * kTile * 128, &p.q, c * 64,
+                                x.t.first_q + x.t.row + t * kTile, x.hq, bar);
+                return true;
+            };
+            auto load_k = [&](int j) {
+                for (int c = 0; c < C::Pieces; ++c) {
+                    uint32_t dst, bar;
+                    if (!next(dst, bar)) return false;
+                    for (int e = 0; e < C::QBlocks / C::Pieces; ++e)
+                        tma_load_3d(dst + e * kTile * 128, &p.k, (c * (C::QBlocks / C::Pieces) + e) * 64,
+                                    x.t.first_k + j * kTile, h, bar);
+                }
+                return true;
+            };
+            auto load_v = [&](int j) {
+                for (int c = 0; c < C::Pieces; ++c) {
+                    uint32_t dst, bar;
+                    if (!next(dst, bar)) return false;
+                    for (int e = 0; e < C::QBlocks; ++e)
+                        tma_load_3d(dst + e * C::VKeys * 128, &p.v, e * 64, x.t.first_k + j * kTile + c * C::VKeys, h,
+                                    bar);
+                }
+                return true;
+            };
+            // in the order the products take them
+            if (C::NQ == 2) {
+                ok = load_q(0) && (x.most == 0 || load_k(0)) && load_q(1);
+                for (int j = 0; ok && j < x.most; ++j) ok = load_v(j) && (j + 1 >= x.most || load_k(j + 1));
+            } else {
+                ok = load_q(0) && (x.most < 1 || load_k(0)) && (x.most < 2 || load_k(1));
+                for (int j = 0; ok && j < x.most; ++j) ok = load_v(j) && (j + 2 >= x.most || load_k(j + 2));
+            }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+    }
+    if (lane == 0) {                                           // every load lands before the CTA exits
+        for (uint32_t k = 0; k < C::Stages && k < pieces; ++k) {
+            const uint32_t j = pieces - 1 - k;
+            mbar_wait(smem_u32(&B.full[j % C::Stages]), (j / C::Stages) & 1);
+        }
+        for (int t = 0; t < C::NQ; ++t)
+            if (q_count[t] > 0) mbar_wait(smem_u32(&B.q_full[t]), (q_count[t] - 1) & 1);
+    }
+}
+
+template <int D, bool kBF16>
+__device__ void mma_role(const Params &p, Book &B, uint8_t *ring_ptr, uint32_t q_smem, uint32_t ring, uint32_t tmem)
+{
+    using C = Cfg<D>;
+    constexpr uint32_t kFmt = kBF16 ? kFmtBF16 : kFmtF16;
+    constexpr uint32_t kIdS = idesc(kAccF32, kFmt, kFmt, kTile, kTile);
+    constexpr uint32_t kIdO = idesc(kAccF32, kFmt, kFmt, kTile, D) | kBMajorMN;
+    const int lane = threadIdx.x & 31;
+    const int64_t items = static_cast<int64_t>(p.tiles) * p.s.heads * p.s.group;
+    uint32_t pieces = 0, q_count[2] = {0, 0}, p_count[2] = {0, 0};
+    bool ok = true;
+    auto wait = [&](uint64_t &bar, uint32_t parity, unsigned what) {
+        if (mbar_wait_warp(smem_u32(&bar), parity)) return true;
+        if (lane == 0) atomicOr(&g_status, what);
+        return false;
+    };
+    auto wait_piece = [&](uint32_t k) { return wait(B.full[k % C::Stages], (k / C::Stages) & 1, kErrTimeoutLoad); };
+    auto release = [&](uint32_t k) {
+        if (lane == 0) mma_commit(smem_u32(&B.empty[k % C::Stages]));
+    };
+    // S of `buf` = query tile t times the K tile whose pieces start at k
+    auto score = [&](int t, int buf, uint32_t k, bool last) {
+        constexpr int kBlocks = C::QBlocks / C::Pieces;
+        for (int c = 0; c < C::Pieces; ++c) {
+            if (!wait_piece(k + c)) return false;
+            tc_fence_after_sync();
+            if (lane == 0) {
+                const uint32_t kb = ring + ((k + c) % C::Stages) * C::PieceBytes;
+                const uint32_t qb = q_smem + t * C::QBytes + c * kBlocks * kTile * 128;
+#pragma unroll
+                for (int e = 0; e < kBlocks * 4; ++e) {
+                    const uint32_t off = (e >> 2) * kTile * 128 + (e & 3) * 32;
+                    mma_f16_ss(tmem + buf * kTile, desc_k_sw128(qb + off), desc_k_sw128(kb + off), kIdS, c + e > 0);
+                }
+            }
+            if (last) release(k + c);
+        }
+        if (lane == 0) mma_commit(smem_u32(&B.s_full[buf]));
+        return true;
+    };
+    // O of query tile t (+)= P of `buf` times the V tile whose pieces start at k;
+    // keys: its keys that belong to the sequence; fresh: the tile's first use
+    auto weigh = [&](int t, int buf, uint32_t k, int keys, bool first, bool fresh, bool last) {
+        if (!wait(B.p_full[buf], p_count[buf] & 1, kErrTimeoutDrain)) return false;
+        ++p_count[buf];
+        for (int c = 0; c < C::Pieces; ++c) {
+            if (!wait_piece(k + c)) return false;
+            const uint32_t off = ((k + c) % C::Stages) * C::PieceBytes;
+            if (fresh && keys < (c + 1) * C::VKeys) {
+                // rows behind the sequence are weighed with 0: clear them, lest they hold NaN
+                const int from = max(keys - c * C::VKeys, 0);
+                for (int e = 0; e < C::QBlocks; ++e) {
+                    uint4 *rows = reinterpret_cast<uint4 *>(ring_ptr + off + e * C::VKeys * 128);
+                    for (int y = from * 8 + lane; y < C::VKeys * 8; y += 32) rows[y] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            tc_fence_after_sync();
+            if (lane == 0) {
+#pragma unroll
+                for (int e = 0; e < C::VKeys / 16; ++e)
+                    mma_f16_ts(tmem + C::OCol + t * D, tmem + buf * kTile + (c * C::VKeys / 16 + e) * 8,
+                               desc_mn_sw128(ring + off + e * 2048, C::VKeys * 128), kIdO, !first || c + e > 0);
+            }
+            if (last) release(k + c);
+        }
+        if (lane == 0) mma_commit(smem_u32(&B.o_done[t]));
+        return true;
+    };
+    auto wait_q = [&](int t) {
+        if (!wait(B.q_full[t], q_count[t] & 1, kErrTimeoutLoad)) return false;
+        ++q_count[t];
+        return true;
+    };
+    auto free_q = [&](int t) {
+        if (lane == 0) mma_commit(smem_u32(&B.q_empty[t]));
+    };
+    for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+        Item x;
+        if (!item_at<D>(p, i, x)) break;
+        const int len = x.t.len_k;
+        if constexpr (C::NQ == 2) {
+            // pieces in order: K0, V0, K1, V1, ...; a tile is last used by query
+            // tile 1 unless that one has fewer tiles
+            const bool two = x.n[1] > 0;
+            for (int t = 0; ok && t < 2; ++t) {
+                if (x.n[t] == 0) continue;
+                ok = wait_q(t) && score(t, t, pieces, t == 1 || !two);
+                if (x.n[t] == 1) free_q(t);
+            }
+            for (int j = 0; ok && j < x.most; ++j) {
+                const uint32_t v = pieces + 2 * j + 1, k = v + 1;
+                for (int t = 0; ok && t < 2; ++t) {
+                    if (j >= x.n[t]) continue;
+                    ok = weigh(t, t, v, len - j * kTile, j == 0, t == 0 || j >= x.n[0], t == 1 || !two);
+                    if (ok && j + 1 < x.n[t]) {
+                        ok = score(t, t, k, t == 1 || !two);
+                        if (j + 2 == x.n[t]) free_q(t);
+                    }
+                }
+            }
+            pieces += 2 * x.most;
+        } else {
+            // K0 K1 V0 K2 V1 ...: tile j's K is the (j < 2 ? j : 2 j - 1)-th tile of the
+            // ring, its V the one after K of tile j + 1
+            if (x.most == 0) continue;
+            const int n = x.most;
+            auto k_tile = [&](int j) { return pieces + C::Pieces * (j < 2 ? j : 2 * j - 1); };
+            auto v_tile = [&](int j) { return pieces + C::Pieces * (j + min(j + 2, n)); };
+            ok = wait_q(0) && score(0, 0, k_tile(0), true) && (n < 2 || score(0, 1, k_tile(1), true));
+            if (n <= 2) free_q(0);
+            for (int j = 0; ok && j < n; ++j) {
+                ok = weigh(0, j & 1, v_tile(j), len - j * kTile, j == 0, true, true);
+                if (ok && j + 2 < n) {
+                    ok = score(0, j & 1, k_tile(j + 2), true);
+                    if (j + 3 == n) free_q(0);
+                }
+            }
+            pieces += 2 * C::Pieces * n;
+        }
+    }
+    // all products complete before the tensor memory is freed
+    if (lane == 0) mma_commit(smem_u32(&B.drain));
+    __syncwarp();
+    mbar_wait_warp(smem_u32(&B.drain), 0);
+}
+
+template <int D, bool kBF16>
+__global__ void __launch_bounds__(Cfg<D>::Threads, 1) prompt_tc_kernel(const __grid_constant__ Params p)
+{
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Book B;
+    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t *ring_ptr = smem + C::NQ * C::QBytes;
+    const uint32_t q_smem = smem_u32(smem), ring = smem_u32(ring_ptr);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == C::WarpTma && lane == 0) {
+        for (int s = 0; s < C::Stages; ++s) {
+            mbar_init(smem_u32(&B.full[s]), 1);
+            mbar_init(smem_u32(&B.empty[s]), 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(smem_u32(&B.q_full[t]), 1);
+            mbar_init(smem_u32(&B.q_empty[t]), 1);
+            mbar_init(smem_u32(&B.s_full[t]), 1);
+            mbar_init(smem_u32(&B.p_full[t]), 4);
+            mbar_init(smem_u32(&B.o_done[t]), 1);
+        }
+        mbar_init(smem_u32(&B.drain), 1);
+        fence_mbar_init();
+        prefetch_tensormap(&p.q);
+        prefetch_tensormap(&p.k);
+        prefetch_tensormap(&p.v);
+    }
+    if (warp == C::WarpMma) {
+        tmem_alloc(smem_u32(&B.tmem_base), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = B.tmem_base;
+    if (warp < C::SoftmaxWarps) {
+        if constexpr (C::NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SoftmaxRegs));
+        softmax_role<D, kBF16>(p, B, warp >> 2, tmem);
+    } else {
+        if constexpr (C::NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OtherRegs));
+        if (warp == C::WarpTma) tma_role<D>(p, B, q_smem, ring);
+        else if (warp == C::WarpMma) mma_role<D, kBF16>(p, B, ring_ptr, q_smem, ring, tmem);
+    }
+    __syncwarp();
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == C::WarpMma) tmem_dealloc(tmem, 512);
+}
+
+// (heads, rows, d) tensor of 16-bit elements, box of 64 elements x `box` rows
+bool make_map(CUtensorMap *map, const void *base, int dtype, int d, int rows, int heads, int64_t head, int64_t row,
+              int box)
+{
+    const EncodeTiledFn encode = encode_tiled();
+    if (!encode) return false;
+    if (heads == 1) head = static_cast<int64_t>(rows) * row;   // unused
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(heads)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row) * 2, static_cast<cuuint64_t>(head) * 2};
+    const cuuint32_t b[3] = {64, static_cast<cuuint32_t>(box), 1}, es[3] = {1, 1, 1};
+    return encode(map, dtype == AXR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                  const_cast<void *>(base), dims, strides, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool kBF16>
+cudaError_t launch(Params &p, const PromptArgs &a, cudaStream_t stream)
+{
+    using C = Cfg<D>;
+    static std::atomic<unsigned long long> done{0};
+    const auto kernel = prompt_tc_kernel<D, kBF16>;
+    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), smem_bytes<D>() - sizeof(Book), done);
+    if (e != cudaSuccess) return e;
+    p.tiles = prompt_tiles(a.s, C::BM);
+    p.scale = kLog2e / sqrtf(static_cast<float>(D));
+    const int64_t items = static_cast<int64_t>(p.tiles) * a.s.heads * a.s.group;
+    const int sms = device_sm_count();
+    kernel<<<items < sms ? static_cast<int>(items) : sms, C::Threads, smem_bytes<D>() - sizeof(Book), stream>>>(p);
+    return cudaGetLastError();
+}
+
+bool make_params(const PromptArgs &a, Params &p)
+{
+    const PromptShape &s = a.s;
+    const int hq = s.heads * s.group;
+    if (!make_map(&p.q, a.q, a.dtype, a.d, s.total_q, hq, s.q_head, s.q_row, kTile) ||
+        !make_map(&p.k, a.K, a.dtype, a.d, s.total_k, s.heads, s.k_head, s.k_row, kTile) ||
+        !make_map(&p.v, a.V, a.dtype, a.d, s.total_k, s.heads, s.v_head, s.v_row, a.d == 256 ? kTile / 2 : kTile))
+        return false;
+    p.s = s;
+    p.out = a.out;
+    p.lse = a.lse;
+    AXR_DEBUG_ONLY(p.sp_out = dbg::span(a.out, ((hq - 1) * s.o_head + (s.total_q - 1) * s.o_row + a.d) * 2);
+                   p.sp_lse = dbg::span(a.lse, a.lse ? 4ull * hq * s.total_q : 0);
+                   p.sp_cu_q = dbg::span(s.cu_q, 4ull * (s.batch + 1));
+                   p.sp_cu_k = dbg::span(s.cu_k, 4ull * (s.batch + 1));)
+    return true;
+}
+
+// what a tensor map takes: strides up to 2^40 bytes, none 0
+bool strides_fit(int heads, int64_t head, int64_t row)
+{
+    constexpr int64_t kMost = int64_t{1} << 38;
+    return row < kMost && (heads == 1 || (head > 0 && head < kMost));
+}
+
+}  // namespace
+
+bool prompt_tc_supported(const PromptArgs &a)
+{
+    const PromptShape &s = a.s;
+    return a.dtype != AXR_F32 && (a.d == 64 || a.d == 128 || a.d == 256) && s.total_k > 0 && encode_tiled() &&
+           strides_fit(s.heads * s.group, s.q_head, s.q_row) && strides_fit(s.heads, s.k_head, s.k_row) &&
+           strides_fit(s.heads, s.v_head, s.v_row);
+}
+
+cudaError_t launch_prompt_attention_tc(const PromptArgs &a, cudaStream_t stream)
+{
+    Params p{};
+    if (!make_params(a, p)) return cudaErrorInvalidValue;
+    const bool bf16 = a.dtype == AXR_BF16;
+    switch (a.d) {
+    case 64: return bf16 ? launch<64, true>(p, a, stream) : launch<64, false>(p, a, stream);
+    case 128: return bf16 ? launch<128, true>(p, a, stream) : launch<128, false>(p, a, stream);
+    default: return bf16 ? launch<256, true>(p, a, stream) : launch<256, false>(p, a, stream);
+    }
+}
+
+unsigned int prompt_tc_status(bool clear)
+{
+    unsigned int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_status, sizeof(v)) != cudaSuccess) return ~0u;
+    if (clear && v) {
+        const unsigned int z = 0;
+        cudaMemcpyToSymbol(g_status, &z, sizeof(z));
+    }
+    return v;
+}
+
+}  // namespace axr

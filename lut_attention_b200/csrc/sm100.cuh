@@ -145,6 +145,16 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// 3-D tiled TMA load of one box
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
 // 1-D tiled TMA load (x: element index, a multiple of 16 bytes' worth of elements)
 __device__ __forceinline__ void tma_load_1d(uint32_t dst, const CUtensorMap *map, int x, uint32_t bar)
 {
@@ -205,6 +215,20 @@ __device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uin
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}"
         ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate),
+          "r"(0u), "r"(0u), "r"(0u), "r"(0u)
+        : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem desc]^T, kind::f16; A holds two 16-bit elements
+// of its row in every 32-bit column
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate),
           "r"(0u), "r"(0u), "r"(0u), "r"(0u)
         : "memory");
 }
@@ -341,6 +365,22 @@ __device__ __forceinline__ uint64_t desc_k_sw128(uint32_t addr)
     d |= static_cast<uint64_t>(2) << 61;                        // layout: 128-byte swizzle
     return d;
 }
+
+// MN-major operand (the M or N index runs along the 128-byte rows, K across them)
+// in 128-byte-swizzled rows: 64 elements of 16 bits per row, 8-row atoms of 1024
+// bytes along K.  `addr` is the row of the first K index (a multiple of 8 rows),
+// `block` the byte distance between 64-element blocks along M or N.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr, uint32_t block)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((addr >> 4) & 0x3fff);
+    d |= static_cast<uint64_t>((block >> 4) & 0x3fff) << 16;    // leading byte offset: next 64 along M or N
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;                // stride byte offset: next 8 along K
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+constexpr uint32_t kBMajorMN = 1u << 16;    // instruction descriptor: B is MN-major
 
 // K-major operand without swizzle: 8-row x 16-byte core matrices.
 // lbo = byte distance between K-adjacent core matrices, sbo = between
