@@ -31,7 +31,8 @@ DEBUG_LIB_PATH = os.path.join(PKG, "libaxr_debug.so")
 
 SOURCES = ["api.cu", "attention.cu", "cache_evict.cu", "codebook.cpp", "prompt_attention.cu",
            "prompt_attention_tc.cu", "quantize_keys.cu", "quantize_keys_block.cu", "quantize_keys_tc.cu", "scores.cu",
-           "scores_tc.cu", "scores_tc128.cu", "shared_attention.cu", "sign_select.cu"]
+           "scores_tc.cu", "scores_tc128.cu", "shared_attention.cu",
+           "shared_attention_tc.cu", "sign_select.cu"]
 HEADERS = [os.path.join(INCLUDE, "axr.h")] + [
     os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))
 ]

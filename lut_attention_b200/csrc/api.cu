@@ -675,10 +675,10 @@ extern "C" int axr_device_status(int clear, unsigned int *status)
     if (e != cudaSuccess) return fail(AXR_ECUDA, "device synchronize: %s", cudaGetErrorString(e));
     const unsigned int q = quantize_tc_status(clear != 0);
     const unsigned int r = scores_tc_status(clear != 0);
-    const unsigned int t = prompt_tc_status(clear != 0);
+    const unsigned int t = prompt_tc_status(clear != 0), s = shared_tc_status(clear != 0);
     const unsigned int bnd = dbg::read_all(clear != 0);
-    if (q == ~0u || r == ~0u || t == ~0u || bnd == ~0u) return fail(AXR_ECUDA, "reading the device status words failed");
-    *status = q | r | t | bnd;
+    if (q == ~0u || r == ~0u || t == ~0u || s == ~0u || bnd == ~0u) return fail(AXR_ECUDA, "reading the device status words failed");
+    *status = q | r | t | s | bnd;
     return ok();
 }
 

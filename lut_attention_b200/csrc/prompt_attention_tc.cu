@@ -33,16 +33,15 @@
 #include "axr_internal.cuh"
 #include "prompt.cuh"
 #include "sm100.cuh"
+#include "softmax_tc.cuh"
 
 namespace axr {
 namespace {
 
 using namespace sm100;
+using namespace softmax;
 
 constexpr int kTile = 128;                     // queries of a tile, keys of a tile
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLazy = 8.0f;                  // log2 of the growth that rescales
 constexpr int kMaxStages = 12;
 
 __device__ unsigned int g_status;
@@ -59,11 +58,7 @@ struct Cfg {
     static constexpr int Stages = D == 64 ? 11 : 5;
     static constexpr int SoftmaxWarps = 4 * NQ;
     static constexpr int WarpMma = SoftmaxWarps, WarpTma = SoftmaxWarps + 1;
-    // two query tiles: a third warpgroup (TMA, MMA, two idle warps) hands registers
-    // to the softmax warps, of the 168 a thread that 384 threads get at launch
-    static constexpr int Threads = NQ == 2 ? 384 : 192;
-    static constexpr int SoftmaxRegs = 224, OtherRegs = 56;
-    static_assert(2 * SoftmaxRegs + OtherRegs <= 3 * 168, "registers of the block");
+    static constexpr int Threads = (SoftmaxWarps + 2) * 32;
     static constexpr int OCol = 2 * kTile;                     // S buffers first, then O
     static_assert(OCol + NQ * D <= 512, "tensor memory");
     static_assert(Stages <= kMaxStages, "ring");
@@ -73,7 +68,7 @@ struct Book {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2];        // S of a buffer is complete
-    uint64_t p_full[2];        // its P is written (and O rescaled where needed)
+    uint64_t p_full[2][2];     // the first and second half of its P is written (and O rescaled where needed)
     uint64_t o_done[2];        // a query tile's latest P V is complete
     uint64_t drain;
     uint32_t tmem_base;
@@ -121,72 +116,6 @@ __device__ __forceinline__ bool item_at(const Params &p, int64_t i, Item &x)
     return true;
 }
 
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint64_t pair(float a, float b)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpair(uint64_t v, float &a, float &b)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-// two weights as packed 16-bit values, the first in the low half
-template <bool kBF16>
-__device__ __forceinline__ uint32_t pack16(float a, float b)
-{
-    uint32_t r;
-    if constexpr (kBF16) asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(a), "f"(b));
-    else asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(a), "f"(b));
-    return r;
-}
-
-// fp16 weights carry a factor 2^7: with the lazy maximum they reach 2^15 at most,
-// and those as small as 2^-21 of the largest are still normal numbers
-template <bool kBF16>
-constexpr float kBias = kBF16 ? 0.0f : 7.0f;
-
-// Softmax of 64 scores: p = 2^(s * scale + c), their sum into (sum0, sum1), packed into w
-template <bool kBF16>
-__device__ __forceinline__ void weights64(const uint32_t (&s)[64], uint64_t scale2, uint64_t c2, uint64_t &sum0,
-                                          uint64_t &sum1, uint32_t (&w)[32])
-{
-#pragma unroll
-    for (int i = 0; i < 64; i += 4) {
-        float a, b, c, d;
-        unpair(fma2(pair(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), scale2, c2), a, b);
-        unpair(fma2(pair(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), scale2, c2), c, d);
-        a = ex2(a);
-        b = ex2(b);
-        c = ex2(c);
-        d = ex2(d);
-        sum0 = add2(sum0, pair(a, b));
-        sum1 = add2(sum1, pair(c, d));
-        w[i / 2] = pack16<kBF16>(a, b);
-        w[i / 2 + 1] = pack16<kBF16>(c, d);
-    }
-}
-
 // The softmax warpgroup of query tile t (buffer t; at NQ = 1 buffers 0 and 1 in
 // turn).  Thread = query.
 template <int D, bool kBF16>
@@ -197,49 +126,39 @@ __device__ void softmax_role(const Params &p, Book &B, int t, uint32_t tmem)
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t o_at = tmem + lanes + C::OCol + t * D;
     const int64_t items = static_cast<int64_t>(p.tiles) * p.s.heads * p.s.group;
-    uint32_t s_count[2] = {0, 0}, o_count = 0;                 // phases of s_full and o_done seen
+    uint32_t count = 0;                                        // tiles so far: phases of s_full and o_done
     for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
         Item x;
         if (!item_at<D>(p, i, x)) break;
-        const int rows = x.rows[t], n = x.n[t];
+        const int rows = t == 0 ? x.rows[0] : x.rows[1], n = t == 0 ? x.n[0] : x.n[1];
         const bool idle = warp * 32 >= rows;                   // no query of this warp
         const int first = x.t.row + t * kTile + warp * 32;     // the warp's first query
         const int past = x.t.len_k - x.t.len_q;
         float m = -INFINITY, l = 0.0f;
-        for (int j = 0; j < n; ++j) {
-            const int buf = C::NQ == 2 ? t : j & 1;
-            if (!mbar_wait_warp(smem_u32(&B.s_full[buf]), s_count[buf] & 1)) {
+        for (int j = 0; j < n; ++j, ++count) {
+            const int buf = C::NQ == 2 ? t : count & 1;
+            if (!mbar_wait_warp_fast(smem_u32(&B.s_full[buf]), (C::NQ == 2 ? count : count >> 1) & 1)) {
                 if (lane == 0) atomicOr(&g_status, kErrTimeoutMma);
                 return;
             }
-            ++s_count[buf];
             if (!idle) {
                 tc_fence_after_sync();
                 const uint32_t s_at = tmem + lanes + buf * kTile;
-                uint32_t a[64], b[64];
-                tmem_ld64(s_at, a);
-                tmem_ld64(s_at + 64, b);
                 const int seen = first + past + 1 - j * kTile; // keys of the tile that the warp's first query sees
-                if (seen < kTile) {
-                    const int lim = seen + lane;
-#pragma unroll
-                    for (int c = 0; c < 64; ++c) {
-                        if (c >= lim) a[c] = 0xff800000u;
-                        if (c + 64 >= lim) b[c] = 0xff800000u;
-                    }
+                const int lim = seen < kTile ? seen + lane : kTile;
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < kTile; c += 32) {
+                    uint32_t s[32];
+                    tmem_ld32(s_at + c, s);
+                    if (seen < kTile) mask32(s, lim - c);
+                    mx = max32(s, mx);
                 }
-                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int c = 0; c < 64; c += 4)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        top[e] = fmaxf(top[e], fmaxf(__uint_as_float(a[c + e]), __uint_as_float(b[c + e])));
-                const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                 if (j == 0) {
                     m = mx;
                 } else if (__any_sync(0xffffffffu, (mx - m) * p.scale > kLazy)) {
                     // the last P V must be complete before O is rescaled
-                    if (!mbar_wait_warp(smem_u32(&B.o_done[t]), (o_count + j - 1) & 1)) {
+                    if (!mbar_wait_warp(smem_u32(&B.o_done[t]), (count - 1) & 1)) {
                         if (lane == 0) atomicOr(&g_status, kErrTimeoutMma);
                         return;
                     }
@@ -248,7 +167,7 @@ __device__ void softmax_role(const Params &p, Book &B, int t, uint32_t tmem)
                     const float f = m == -INFINITY ? 0.0f : ex2((m - up) * p.scale);
                     m = up;
                     l *= f;
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
                         uint32_t o[32];
                         tmem_ld32(o_at + c, o);
@@ -261,26 +180,33 @@ __device__ void softmax_role(const Params &p, Book &B, int t, uint32_t tmem)
                 const float c0 = m == -INFINITY ? 0.0f : kBias<kBF16> - m * p.scale;
                 const uint64_t scale2 = pair(p.scale, p.scale), c2 = pair(c0, c0);
                 uint64_t sum0 = pair(l, 0.0f), sum1 = pair(0.0f, 0.0f);
-                uint32_t w[32];
-                weights64<kBF16>(a, scale2, c2, sum0, sum1, w);
-                tmem_st32(s_at, w);
-                weights64<kBF16>(b, scale2, c2, sum0, sum1, w);
-                tmem_st32(s_at + 32, w);
+#pragma unroll 1
+                for (int c = 0; c < kTile; c += 32) {
+                    uint32_t s[32], w[16];
+                    tmem_ld32(s_at + c, s);
+                    if (seen < kTile) mask32(s, lim - c);
+                    weights32<kBF16>(s, scale2, c2, sum0, sum1, w);
+                    tmem_st16(s_at + c / 2, w);                // over scores that are read already
+                    if ((c & 32) == 0) continue;
+                    // half by half, so that the products of the first run under the second
+                    tmem_wait_st();
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&B.p_full[buf][c >> 6]));
+                }
                 float s0, s1, s2, s3;
                 unpair(sum0, s0, s1);
                 unpair(sum1, s2, s3);
                 l = (s0 + s1) + (s2 + s3);
-                tmem_wait_st();
-                tc_fence_before_sync();
+            } else if (lane == 0) {
+                mbar_arrive(smem_u32(&B.p_full[buf][0]));
+                mbar_arrive(smem_u32(&B.p_full[buf][1]));
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&B.p_full[buf]));
         }
-        o_count += n;
         // the last two P V in turn: with two S buffers both may still be running, and a
         // wait tells a phase only from its neighbours
         for (int k = n < 2 ? n : 2; k > 0; --k)
-            if (!mbar_wait_warp(smem_u32(&B.o_done[t]), (o_count - k) & 1)) {
+            if (!mbar_wait_warp(smem_u32(&B.o_done[t]), (count - k) & 1)) {
                 if (lane == 0) atomicOr(&g_status, kErrTimeoutMma);
                 return;
             }
@@ -290,7 +216,7 @@ __device__ void softmax_role(const Params &p, Book &B, int t, uint32_t tmem)
         const int64_t at = x.t.first_q + x.t.row + t * kTile + r;
         const float inv = l > 0.0f ? 1.0f / l : l;             // 0 for no key, NaN stays NaN
         char *dst = static_cast<char *>(p.out) + (x.hq * p.s.o_head + at * p.s.o_row) * 2;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
             if (n > 0) {
@@ -412,16 +338,16 @@ __device__ void mma_role(const Params &p, Book &B, uint8_t *ring_ptr, uint32_t q
     constexpr uint32_t kIdO = idesc(kAccF32, kFmt, kFmt, kTile, D) | kBMajorMN;
     const int lane = threadIdx.x & 31;
     const int64_t items = static_cast<int64_t>(p.tiles) * p.s.heads * p.s.group;
-    uint32_t pieces = 0, q_count[2] = {0, 0}, p_count[2] = {0, 0};
+    uint32_t pieces = 0, q_count[2] = {0, 0}, p_count[2] = {0, 0};   // indexed by constants only
     bool ok = true;
     auto wait = [&](uint64_t &bar, uint32_t parity, unsigned what) {
-        if (mbar_wait_warp(smem_u32(&bar), parity)) return true;
+        if (mbar_wait_warp_fast(smem_u32(&bar), parity)) return true;
         if (lane == 0) atomicOr(&g_status, what);
         return false;
     };
     auto wait_piece = [&](uint32_t k) { return wait(B.full[k % C::Stages], (k / C::Stages) & 1, kErrTimeoutLoad); };
     auto release = [&](uint32_t k) {
-        if (lane == 0) mma_commit(smem_u32(&B.empty[k % C::Stages]));
+        if (elect_one()) mma_commit(smem_u32(&B.empty[k % C::Stages]));
     };
     // S of `buf` = query tile t times the K tile whose pieces start at k
     auto score = [&](int t, int buf, uint32_t k, bool last) {
@@ -429,7 +355,7 @@ __device__ void mma_role(const Params &p, Book &B, uint8_t *ring_ptr, uint32_t q
         for (int c = 0; c < C::Pieces; ++c) {
             if (!wait_piece(k + c)) return false;
             tc_fence_after_sync();
-            if (lane == 0) {
+            if (elect_one()) {
                 const uint32_t kb = ring + ((k + c) % C::Stages) * C::PieceBytes;
                 const uint32_t qb = q_smem + t * C::QBytes + c * kBlocks * kTile * 128;
 #pragma unroll
@@ -440,14 +366,13 @@ __device__ void mma_role(const Params &p, Book &B, uint8_t *ring_ptr, uint32_t q
             }
             if (last) release(k + c);
         }
-        if (lane == 0) mma_commit(smem_u32(&B.s_full[buf]));
+        if (elect_one()) mma_commit(smem_u32(&B.s_full[buf]));
         return true;
     };
     // O of query tile t (+)= P of `buf` times the V tile whose pieces start at k;
-    // keys: its keys that belong to the sequence; fresh: the tile's first use
-    auto weigh = [&](int t, int buf, uint32_t k, int keys, bool first, bool fresh, bool last) {
-        if (!wait(B.p_full[buf], p_count[buf] & 1, kErrTimeoutDrain)) return false;
-        ++p_count[buf];
+    // phase: that of P; keys: the tile's keys that belong to the sequence; fresh: the
+    // tile's first use
+    auto weigh = [&](int t, int buf, uint32_t phase, uint32_t k, int keys, bool first, bool fresh, bool last) {
         for (int c = 0; c < C::Pieces; ++c) {
             if (!wait_piece(k + c)) return false;
             const uint32_t off = ((k + c) % C::Stages) * C::PieceBytes;
@@ -461,16 +386,21 @@ __device__ void mma_role(const Params &p, Book &B, uint8_t *ring_ptr, uint32_t q
                 fence_proxy_async_smem();
                 __syncwarp();
             }
-            tc_fence_after_sync();
-            if (lane == 0) {
+            constexpr int kHalves = 2 / C::Pieces;             // halves of P that the piece meets
+            for (int h = 0; h < kHalves; ++h) {
+                if (!wait(B.p_full[buf][c * kHalves + h], phase, kErrTimeoutDrain)) return false;
+                tc_fence_after_sync();
+                if (elect_one()) {
 #pragma unroll
-                for (int e = 0; e < C::VKeys / 16; ++e)
-                    mma_f16_ts(tmem + C::OCol + t * D, tmem + buf * kTile + (c * C::VKeys / 16 + e) * 8,
-                               desc_mn_sw128(ring + off + e * 2048, C::VKeys * 128), kIdO, !first || c + e > 0);
+                    for (int e = 0; e < 4; ++e)
+                        mma_f16_ts(tmem + C::OCol + t * D, tmem + buf * kTile + ((c * kHalves + h) * 4 + e) * 8,
+                                   desc_mn_sw128(ring + off + (h * 4 + e) * 2048, C::VKeys * 128), kIdO,
+                                   !first || c + h + e > 0);
+                }
             }
             if (last) release(k + c);
         }
-        if (lane == 0) mma_commit(smem_u32(&B.o_done[t]));
+        if (elect_one()) mma_commit(smem_u32(&B.o_done[t]));
         return true;
     };
     auto wait_q = [&](int t) {
@@ -479,7 +409,7 @@ __device__ void mma_role(const Params &p, Book &B, uint8_t *ring_ptr, uint32_t q
         return true;
     };
     auto free_q = [&](int t) {
-        if (lane == 0) mma_commit(smem_u32(&B.q_empty[t]));
+        if (elect_one()) mma_commit(smem_u32(&B.q_empty[t]));
     };
     for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
         Item x;
@@ -489,16 +419,18 @@ __device__ void mma_role(const Params &p, Book &B, uint8_t *ring_ptr, uint32_t q
             // pieces in order: K0, V0, K1, V1, ...; a tile is last used by query
             // tile 1 unless that one has fewer tiles
             const bool two = x.n[1] > 0;
-            for (int t = 0; ok && t < 2; ++t) {
-                if (x.n[t] == 0) continue;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (!ok || x.n[t] == 0) continue;
                 ok = wait_q(t) && score(t, t, pieces, t == 1 || !two);
                 if (x.n[t] == 1) free_q(t);
             }
             for (int j = 0; ok && j < x.most; ++j) {
                 const uint32_t v = pieces + 2 * j + 1, k = v + 1;
-                for (int t = 0; ok && t < 2; ++t) {
-                    if (j >= x.n[t]) continue;
-                    ok = weigh(t, t, v, len - j * kTile, j == 0, t == 0 || j >= x.n[0], t == 1 || !two);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (!ok || j >= x.n[t]) continue;
+                    ok = weigh(t, t, p_count[t]++ & 1, v, len - j * kTile, j == 0, t == 0 || j >= x.n[0], t == 1 || !two);
                     if (ok && j + 1 < x.n[t]) {
                         ok = score(t, t, k, t == 1 || !two);
                         if (j + 2 == x.n[t]) free_q(t);
@@ -513,20 +445,22 @@ __device__ void mma_role(const Params &p, Book &B, uint8_t *ring_ptr, uint32_t q
             const int n = x.most;
             auto k_tile = [&](int j) { return pieces + C::Pieces * (j < 2 ? j : 2 * j - 1); };
             auto v_tile = [&](int j) { return pieces + C::Pieces * (j + min(j + 2, n)); };
-            ok = wait_q(0) && score(0, 0, k_tile(0), true) && (n < 2 || score(0, 1, k_tile(1), true));
+            const uint32_t at = p_count[0];                    // S buffers in turn over all items
+            ok = wait_q(0) && score(0, at & 1, k_tile(0), true) && (n < 2 || score(0, (at + 1) & 1, k_tile(1), true));
             if (n <= 2) free_q(0);
             for (int j = 0; ok && j < n; ++j) {
-                ok = weigh(0, j & 1, v_tile(j), len - j * kTile, j == 0, true, true);
+                ok = weigh(0, (at + j) & 1, ((at + j) >> 1) & 1, v_tile(j), len - j * kTile, j == 0, true, true);
                 if (ok && j + 2 < n) {
-                    ok = score(0, j & 1, k_tile(j + 2), true);
+                    ok = score(0, (at + j) & 1, k_tile(j + 2), true);
                     if (j + 3 == n) free_q(0);
                 }
             }
+            p_count[0] += n;
             pieces += 2 * C::Pieces * n;
         }
     }
     // all products complete before the tensor memory is freed
-    if (lane == 0) mma_commit(smem_u32(&B.drain));
+    if (elect_one()) mma_commit(smem_u32(&B.drain));
     __syncwarp();
     mbar_wait_warp(smem_u32(&B.drain), 0);
 }
@@ -550,7 +484,8 @@ __global__ void __launch_bounds__(Cfg<D>::Threads, 1) prompt_tc_kernel(const __g
             mbar_init(smem_u32(&B.q_full[t]), 1);
             mbar_init(smem_u32(&B.q_empty[t]), 1);
             mbar_init(smem_u32(&B.s_full[t]), 1);
-            mbar_init(smem_u32(&B.p_full[t]), 4);
+            mbar_init(smem_u32(&B.p_full[t][0]), 4);
+            mbar_init(smem_u32(&B.p_full[t][1]), 4);
             mbar_init(smem_u32(&B.o_done[t]), 1);
         }
         mbar_init(smem_u32(&B.drain), 1);
@@ -568,10 +503,8 @@ __global__ void __launch_bounds__(Cfg<D>::Threads, 1) prompt_tc_kernel(const __g
     tc_fence_after_sync();
     const uint32_t tmem = B.tmem_base;
     if (warp < C::SoftmaxWarps) {
-        if constexpr (C::NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SoftmaxRegs));
         softmax_role<D, kBF16>(p, B, warp >> 2, tmem);
     } else {
-        if constexpr (C::NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OtherRegs));
         if (warp == C::WarpTma) tma_role<D>(p, B, q_smem, ring);
         else if (warp == C::WarpMma) mma_role<D, kBF16>(p, B, ring_ptr, q_smem, ring, tmem);
     }

@@ -79,8 +79,17 @@ struct Run {
     int64_t base;                      // first key row (prefix: head * n, own: (seq * heads + head) * capacity)
 };
 
-// The run that starts at tile t and ends at the segment's end or at `end`.
-__device__ __forceinline__ Run run_at(const Work &w, const Line &x, int64_t t, int64_t end)
+// own keys of sequence b
+__device__ __forceinline__ int length(const Work &w, int b)
+{
+    const int len = AXR_IN(w.sp_lengths, w.lengths + b, 4) ? w.lengths[b] : 0;
+    return min(max(len, 0), w.capacity);
+}
+
+// The run that starts at tile t and ends at the segment's end or at `end`;
+// start(b) is own_start of sequence b, keys(b) its length.
+template <typename Start, typename Keys>
+__device__ __forceinline__ Run run_at(const Work &w, const Line &x, int64_t t, int64_t end, Start start, Keys keys)
 {
     Run r;
     int64_t left;
@@ -99,10 +108,10 @@ __device__ __forceinline__ Run run_at(const Work &w, const Line &x, int64_t t, i
         int lo = 0, hi = w.batch;                             // the last b with heads * own_start[b] <= u
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (static_cast<int64_t>(w.heads) * own_start(w, mid) <= u) lo = mid;
+            if (static_cast<int64_t>(w.heads) * start(mid) <= u) lo = mid;
             else hi = mid;
         }
-        const int s0 = own_start(w, lo), per = own_start(w, lo + 1) - s0;
+        const int s0 = start(lo), per = start(lo + 1) - s0;
         const int64_t v = u - static_cast<int64_t>(w.heads) * s0;
         r.head = static_cast<int>(v / per);
         r.tile = static_cast<int>(v % per);
@@ -110,8 +119,7 @@ __device__ __forceinline__ Run run_at(const Work &w, const Line &x, int64_t t, i
         r.seq = lo;
         r.row0 = 0;
         r.rows = w.group;
-        const int len = AXR_IN(w.sp_lengths, w.lengths + lo, 4) ? w.lengths[lo] : 0;
-        r.keys = min(max(len, 0), w.capacity);
+        r.keys = keys(lo);
         r.seg = static_cast<int64_t>(lo) * w.heads + r.head;
         r.base = r.seg * w.capacity;
     }
@@ -132,6 +140,11 @@ __device__ __forceinline__ float *slot(const Work &w, const Run &r, int cta, int
 {
     if (r.seq >= 0) return w.own_part + ((r.seg + cta) * w.group + i) * (w.d + 2);
     return w.prefix_part + ((r.seg + cta) * w.slot_rows + i) * (w.d + 2);
+}
+
+__device__ __forceinline__ Run run_at(const Work &w, const Line &x, int64_t t, int64_t end)
+{
+    return run_at(w, x, t, end, [&](int b) { return own_start(w, b); }, [&](int b) { return length(w, b); });
 }
 
 // workspace of a call: fills the pointers of w from `base` and returns the bytes
@@ -166,6 +179,11 @@ struct SharedArgs {
 cudaError_t launch_shared_before(const SharedArgs &a, const shared::Work &w, bool halves, cudaStream_t stream);
 cudaError_t launch_shared_after(const SharedArgs &a, const shared::Work &w, cudaStream_t stream);
 int64_t shared_workspace_bytes(int batch, int heads, int group, int d);
+// tensor-core kernel (shared_attention_tc.cu): 16-bit values, d = 64 and 128
+bool shared_tc_supported(const SharedArgs &a);
+shared::Work shared_tc_work(int batch, int heads, int group, int d);
+cudaError_t launch_shared_main_tc(const SharedArgs &a, const shared::Work &w, cudaStream_t stream);
+unsigned int shared_tc_status(bool clear);
 cudaError_t launch_shared_attention(const SharedArgs &a, cudaStream_t stream);
 
 }  // namespace axr

@@ -478,20 +478,27 @@ cudaError_t launch_shared_after(const SharedArgs &a, const Work &w, cudaStream_t
 
 int64_t shared_workspace_bytes(int batch, int heads, int group, int d)
 {
+    // one size for every value type: the larger of the two kernels' needs
     Work w = work_of(batch, heads, group, d);
-    return shared::lay_out(w, nullptr);
+    const int64_t core = shared::lay_out(w, nullptr);
+    if (d != 64 && d != 128) return core;
+    Work t = shared_tc_work(batch, heads, group, d);
+    const int64_t tc = shared::lay_out(t, nullptr);
+    return core > tc ? core : tc;
 }
 
 cudaError_t launch_shared_attention(const SharedArgs &a, cudaStream_t stream)
 {
-    Work w = work_of(a.batch, a.heads, a.group, a.d);
+    const bool tc = shared_tc_supported(a);
+    Work w = tc ? shared_tc_work(a.batch, a.heads, a.group, a.d) : work_of(a.batch, a.heads, a.group, a.d);
     w.n = static_cast<int>(a.n);
     w.capacity = static_cast<int>(a.capacity);
     w.lengths = a.lengths;
     shared::lay_out(w, a.workspace);
-    cudaError_t e = launch_shared_before(a, w, false, stream);
+    cudaError_t e = launch_shared_before(a, w, tc, stream);
     if (e != cudaSuccess) return e;
-    switch (a.d) {
+    if (tc) e = launch_shared_main_tc(a, w, stream);
+    else switch (a.d) {
     case 32: e = launch_main_d<32>(a, w, stream); break;
     case 64: e = launch_main_d<64>(a, w, stream); break;
     case 128: e = launch_main_d<128>(a, w, stream); break;

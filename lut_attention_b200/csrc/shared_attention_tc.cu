@@ -1,0 +1,667 @@
+// Main kernel of the shared-prefix decode attention on the 5th-generation tensor
+// cores (axr_attention_shared for 16-bit values, d = 64 and 128).  Per tile of 128
+// keys and up to 128 queries (a block of the batch * group queries of a KV head
+// against the prefix, or the group's queries against a sequence's own keys):
+//     S = (Q_hi + Q_lo) C^T              C: the keys' centroids, fp16 in shared memory
+//     x_t = S_t norm_t,  p = 2^(x rs - m)  one thread per query, fp32
+//     O += P V,  l += sum p                O in tensor memory, P of V's type
+// rs holds the query's own factor and the codebook's (half_codebook.h).  The keys
+// are looked up once for all 128 queries and never multiplied out: a code becomes
+// its centroid, 16 bits picked out of at most 8 by byte permutes, and the norm
+// joins after the product.  The query is split into two fp16 parts (22 bits), so
+// that only the centroids' rounding (at most 2^-13 relatively) is left in S.
+//
+// A persistent CTA per SM walks its stretch of tiles (shared.cuh) with
+//   warps 0-3   softmax: Q into tensor memory (an operand from there, which spares
+//               shared memory), the weights, and a run's end into its slot;
+//   warps 4-7   codes to centroids: thread = key, its packed row loaded one tile
+//               ahead, 16-byte stores in the swizzled rows the products read;
+//   warp 8      products: S of the tile after next is issued before P V of this one,
+//               so the tensor cores run under the softmax;
+//   warp 9      TMA loads of V, a ring of tiles.
+// Rows of V behind a sequence's length may hold anything; they are cleared in
+// shared memory, since 0 times NaN is NaN.
+//
+// Bound: the codes, norms and values of a tile are 128 (P + 4 + 2d) bytes, 41 KB at
+// d = 128 and b = 4, about 1800 cycles of one SM's share of the memory bandwidth;
+// its products take 3 * 512.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <mutex>
+
+#include "axr_internal.cuh"
+#include "half_codebook.h"
+#include "shared.cuh"
+#include "sm100.cuh"
+#include "softmax_tc.cuh"
+
+namespace axr {
+namespace {
+
+using namespace sm100;
+using namespace softmax;
+using shared::Line;
+using shared::Run;
+using shared::Work;
+
+constexpr int kTile = shared::kTileKeys;
+constexpr int kQueries = 128;
+constexpr int kThreads = 384;                  // three warpgroups: softmax, codes, products and loads
+constexpr int kWarpMma = 8, kWarpTma = 9;
+// of the 168 registers a thread that 384 threads get at launch
+constexpr int kSoftmaxRegs = 232, kOtherRegs = 104;
+static_assert(kSoftmaxRegs + 168 + kOtherRegs <= 3 * 168, "registers of the block");
+constexpr int kIndexed = 1024;                 // sequences whose starts and lengths fit shared memory
+
+__device__ unsigned int g_status;
+
+template <int D>
+struct Cfg {
+    static constexpr int Blocks = D / 64;                      // 64-element blocks of a row
+    static constexpr int TileBytes = kTile * D * 2;            // centroids or values of a tile
+    static constexpr int KStages = 2;
+    static constexpr int VStages = D == 64 ? 8 : 4;
+    static constexpr int OCol = 2 * kTile, QCol = OCol + D;    // tensor memory: two S, O, Q
+    static_assert(QCol + D <= 512, "tensor memory");
+};
+constexpr int kMaxV = 8;
+
+struct Book {
+    uint64_t v_full[kMaxV], v_empty[kMaxV];
+    uint64_t k_full[2], k_empty[2];
+    uint64_t s_full[2], p_full[2];
+    uint64_t n_full[4];        // norms of a tile are written
+    uint64_t q_full, o_done, drain;
+    uint32_t tmem_base;
+    alignas(16) float norms[4][kTile];                         // read 16 bytes at a time
+    int32_t start[kIndexed + 1], len[kIndexed];
+};
+
+template <int D>
+constexpr size_t smem_bytes() { return 1024 + (Cfg<D>::KStages + Cfg<D>::VStages) * Cfg<D>::TileBytes; }
+static_assert(smem_bytes<128>() + sizeof(Book) <= 232448 && smem_bytes<64>() + sizeof(Book) <= 232448, "shared memory");
+
+struct Params {
+    CUtensorMap prefix_v, own_v;       // (heads, rows, d), box 64 x 128 rows
+    Work w;
+    const uint8_t *prefix_idx, *idx;
+    const float *prefix_norms, *norms;
+    float inv_scale;                   // 1 / the codebook's scale
+    // centroids by code: low and high bytes (b = 4: magnitudes of codes 8 .. 15)
+    uint32_t lo[2], hi[2];
+    AXR_DEBUG_ONLY(dbg::Span sp_prefix_idx, sp_idx, sp_prefix_norms, sp_norms;)
+};
+
+// Walks a CTA's tiles, run by run.
+struct Cursor {
+    const Work &w;
+    const Book &B;
+    Line x;
+    int64_t t, end;
+    Run r;
+    int k = 0;                         // tiles of the run passed
+    bool more;
+
+    __device__ Cursor(const Work &work, const Book &book) : w(work), B(book), x(shared::line_of(work))
+    {
+        t = blockIdx.x < x.ctas ? x.begin(blockIdx.x) : 0;
+        end = blockIdx.x < x.ctas ? x.begin(blockIdx.x + 1) : 0;
+        find();
+    }
+    __device__ void find()
+    {
+        more = t < end;
+        k = 0;
+        if (!more) return;
+        if (w.batch <= kIndexed) r = shared::run_at(w, x, t, end, [&](int b) { return B.start[b]; }, [&](int b) { return B.len[b]; });
+        else r = shared::run_at(w, x, t, end);
+    }
+    __device__ void next_run()
+    {
+        t += r.tiles;
+        find();
+    }
+    __device__ void next()
+    {
+        if (++k == r.tiles) next_run();
+    }
+    __device__ int tile() const { return r.tile + k; }                         // in its segment
+    __device__ int keys() const { return min(kTile, r.keys - tile() * kTile); }
+};
+
+// 32 scores of this thread's query times the keys' norms
+__device__ __forceinline__ void scaled32(uint32_t at, const float *norms, uint32_t (&s)[32])
+{
+    tmem_ld32(at, s);
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+        const float4 n = *reinterpret_cast<const float4 *>(norms + e);
+        float a, b;
+        unpair(mul2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), pair(n.x, n.y)), a, b);
+        s[e] = __float_as_uint(a);
+        s[e + 1] = __float_as_uint(b);
+        unpair(mul2(pair(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), pair(n.z, n.w)), a, b);
+        s[e + 2] = __float_as_uint(a);
+        s[e + 3] = __float_as_uint(b);
+    }
+}
+
+template <int D, bool kBF16>
+__device__ void softmax_role(const Params &p, Book &B, uint32_t tmem)
+{
+    using C = Cfg<D>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t o_at = tmem + lanes + C::OCol, q_at = tmem + lanes + C::QCol;
+    const int row = threadIdx.x;                               // query of the run
+    auto fail = [&](unsigned what) {
+        if (lane == 0) atomicOr(&g_status, what);
+    };
+    // the run's rotated queries (d high parts, d low parts, fp16) into tensor memory
+    auto load_q = [&](const Run &r) {
+        const bool live = row < r.rows;
+        const int64_t q = live ? shared::query_row(p.w, r, row) : 0;
+        const uint4 *src = static_cast<const uint4 *>(p.w.rot) + q * (D / 4);
+        if (warp * 32 < r.rows) {
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                uint32_t v[32];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    uint4 y = make_uint4(0u, 0u, 0u, 0u);
+                    if (live && AXR_IN(p.w.sp_rot, src + c / 4 + e, 16)) y = src[c / 4 + e];
+                    v[4 * e] = y.x; v[4 * e + 1] = y.y; v[4 * e + 2] = y.z; v[4 * e + 3] = y.w;
+                }
+                tmem_st32(q_at + c, v);
+            }
+            tmem_wait_st();
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&B.q_full));
+        const float *rs = p.w.rot_scale + q;
+        return live && AXR_IN(p.w.sp_rot_scale, rs, 4) ? *rs * p.inv_scale : 0.0f;
+    };
+    Cursor c(p.w, B);
+    if (!c.more) return;
+    float rs = load_q(c.r), rs_next = 0.0f;
+    uint32_t i = 0;                                            // tiles of the CTA so far
+    while (c.more) {
+        const Run r = c.r;
+        const bool idle = warp * 32 >= r.rows;                 // no query of this warp
+        float m = -INFINITY, l = 0.0f;
+        for (int k = 0; k < r.tiles; ++k, ++i) {
+            const int buf = i & 1;
+            if (!mbar_wait_warp(smem_u32(&B.s_full[buf]), (i >> 1) & 1)) return fail(kErrTimeoutMma);
+            tc_fence_after_sync();
+            if (k + 1 == r.tiles) {                            // all products with this run's Q are done
+                c.next_run();
+                if (c.more) rs_next = load_q(c.r);
+            }
+            if (!mbar_wait_warp(smem_u32(&B.n_full[i & 3]), (i >> 2) & 1)) return fail(kErrTimeoutDrain);
+            if (!idle) {
+                const uint32_t s_at = tmem + lanes + buf * kTile;
+                const float *norms = B.norms[i & 3];
+                const int lim = r.keys - (r.tile + k) * kTile; // keys of the tile
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int e = 0; e < kTile; e += 32) {
+                    uint32_t s[32];
+                    scaled32(s_at + e, norms + e, s);
+                    if (lim < kTile) mask32(s, lim - e);
+                    mx = max32(s, mx);
+                }
+                if (k == 0) {
+                    m = mx;
+                } else if (__any_sync(0xffffffffu, (mx - m) * rs > kLazy)) {
+                    // the last P V must be complete before O is rescaled
+                    if (!mbar_wait_warp(smem_u32(&B.o_done), (i - 1) & 1)) return fail(kErrTimeoutMma);
+                    tc_fence_after_sync();
+                    const float up = fmaxf(m, mx);
+                    const float f = m == -INFINITY ? 0.0f : ex2((m - up) * rs);
+                    m = up;
+                    l *= f;
+#pragma unroll 1
+                    for (int e = 0; e < D; e += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o_at + e, o);
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                        tmem_st32(o_at + e, o);
+                    }
+                }
+                const float c0 = m == -INFINITY ? 0.0f : kBias<kBF16> - m * rs;
+                const uint64_t scale2 = pair(rs, rs), c2 = pair(c0, c0);
+                uint64_t sum0 = pair(l, 0.0f), sum1 = pair(0.0f, 0.0f);
+#pragma unroll 1
+                for (int e = 0; e < kTile; e += 32) {
+                    uint32_t s[32], w[16];
+                    scaled32(s_at + e, norms + e, s);
+                    if (lim < kTile) mask32(s, lim - e);
+                    weights32<kBF16>(s, scale2, c2, sum0, sum1, w);
+                    tmem_st16(s_at + e / 2, w);                // over scores that are read already
+                }
+                float s0, s1, s2, s3;
+                unpair(sum0, s0, s1);
+                unpair(sum1, s2, s3);
+                l = (s0 + s1) + (s2 + s3);
+                tmem_wait_st();
+                tc_fence_before_sync();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&B.p_full[buf]));
+        }
+        // the last two P V in turn: both may still be running, and a wait tells a phase
+        // only from its neighbours
+        if (i > 1 && !mbar_wait_warp(smem_u32(&B.o_done), (i - 2) & 1)) return fail(kErrTimeoutMma);
+        if (!mbar_wait_warp(smem_u32(&B.o_done), (i - 1) & 1)) return fail(kErrTimeoutMma);
+        if (!idle) {
+            tc_fence_after_sync();
+            float *dst = shared::slot(p.w, r, blockIdx.x, row);
+            const bool live = row < r.rows && AXR_IN((r.seq >= 0 ? p.w.sp_own_part : p.w.sp_prefix_part), dst, (D + 2) * 4);
+#pragma unroll
+            for (int e = 0; e < D; e += 32) {
+                uint32_t o[32];
+                tmem_ld32(o_at + e, o);
+                if (live) {
+#pragma unroll
+                    for (int y = 0; y < 32; y += 2)
+                        *reinterpret_cast<uint2 *>(dst + e + y) = make_uint2(o[y], o[y + 1]);
+                }
+            }
+            if (live) *reinterpret_cast<float2 *>(dst + D) = make_float2(m == -INFINITY ? m : m * rs - kBias<kBF16>, l);
+            tc_fence_before_sync();
+        }
+        rs = rs_next;
+    }
+}
+
+// Eight codes (8 B bits in the low bits of w) as eight nibbles.
+template <int B>
+__device__ __forceinline__ uint32_t nibbles(uint32_t w)
+{
+    if constexpr (B == 3) {
+        w = (w & 0x00000fffu) | ((w << 4) & 0x0fff0000u);
+        w = (w & 0x003f003fu) | ((w << 2) & 0x3f003f00u);
+        w = (w & 0x07070707u) | ((w << 1) & 0x70707070u);
+    } else if constexpr (B == 2) {
+        w = (w & 0x000000ffu) | ((w << 8) & 0x00ff0000u);
+        w = (w & 0x000f000fu) | ((w << 4) & 0x0f000f00u);
+        w = (w & 0x03030303u) | ((w << 2) & 0x30303030u);
+    } else if constexpr (B == 1) {
+        w = (w & 0x0000000fu) | ((w << 12) & 0x000f0000u);
+        w = (w & 0x00030003u) | ((w << 6) & 0x03000300u);
+        w = (w & 0x01010101u) | ((w << 3) & 0x10101010u);
+    }
+    return w;
+}
+
+__device__ __forceinline__ uint32_t permute(uint32_t a, uint32_t b, uint32_t sel)
+{
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+    return r;
+}
+
+// The fp16 centroids of eight codes given as nibbles.  Bytes are picked by
+// permutes, four codes at a time, from the table's low and high bytes.  At b = 4
+// the table holds the magnitudes of codes 8 .. 15; code c < 8 is minus that of
+// 15 - c: its three low bits are flipped, and its sign comes from a permute whose
+// selector's top bit (set for c >= 8) replicates the picked byte's sign, 0, while
+// a clear one picks 0x7f.
+template <int B>
+__device__ __forceinline__ uint4 centroids(uint32_t nib, const uint32_t (&lo)[2], const uint32_t (&hi)[2])
+{
+    uint32_t out[4];
+    uint32_t pick = nib;
+    if constexpr (B == 4) {
+        const uint32_t neg = ~nib & 0x88888888u;
+        pick = (nib ^ (neg - (neg >> 3))) & 0x77777777u;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t sel = h ? pick >> 16 : pick;
+        const uint32_t l = permute(lo[0], lo[1], sel);
+        uint32_t u = permute(hi[0], hi[1], sel);
+        if constexpr (B == 4) {
+            const uint32_t s = permute(0x7f7f7f7fu, 0x7f7f7f7fu, h ? nib >> 16 : nib);
+            u |= (s << 1) & 0x80808080u;
+        }
+        out[2 * h] = permute(l, u, 0x5140);
+        out[2 * h + 1] = permute(l, u, 0x7362);
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// Thread = key of the tile.
+template <int D, int B>
+__device__ void code_role(const Params &p, Book &S, uint8_t *k_smem)
+{
+    using C = Cfg<D>;
+    constexpr int P = D * B / 8, W = (P + 3) / 4;              // a packed row in bytes and words
+    const int key = threadIdx.x - 128, lane = threadIdx.x & 31;
+    Cursor c(p.w, S);
+    uint32_t row[W + 1], ahead[W];
+    float norm_ahead = 0.0f;
+    // the packed row and norm of the cursor's tile, zeros past its keys
+    auto fetch = [&](uint32_t (&to)[W], float &norm) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) to[i] = 0u;
+        norm = 0.0f;
+        if (!c.more || key >= c.keys()) return;
+        const bool own = c.r.seq >= 0;
+        const int64_t at = c.r.base + static_cast<int64_t>(c.tile()) * kTile + key;
+        const uint8_t *src = (own ? p.idx : p.prefix_idx) + at * P;
+        const float *ns = (own ? p.norms : p.prefix_norms) + at;
+        if (AXR_IN((own ? p.sp_idx : p.sp_prefix_idx), src, P)) {
+            if constexpr (P % 16 == 0) {
+#pragma unroll
+                for (int i = 0; i < P / 16; ++i) {
+                    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(src) + i);
+                    to[4 * i] = v.x; to[4 * i + 1] = v.y; to[4 * i + 2] = v.z; to[4 * i + 3] = v.w;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < P / 8; ++i) {
+                    const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(src) + i);
+                    to[2 * i] = v.x; to[2 * i + 1] = v.y;
+                }
+            }
+        }
+        if (AXR_IN((own ? p.sp_norms : p.sp_prefix_norms), ns, 4)) norm = __ldcs(ns);
+    };
+    const uint32_t lo[2] = {p.lo[0], p.lo[1]}, hi[2] = {p.hi[0], p.hi[1]};
+    fetch(ahead, norm_ahead);
+    row[W] = 0u;
+    for (uint32_t i = 0; c.more; ++i) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) row[e] = ahead[e];
+        const float norm = norm_ahead;
+        c.next();
+        fetch(ahead, norm_ahead);                              // lands while this tile is looked up
+        const int buf = i & 1;
+        if (!mbar_wait_warp(smem_u32(&S.k_empty[buf]), ((i >> 1) & 1) ^ 1)) {
+            if (lane == 0) atomicOr(&g_status, kErrTimeoutMma);
+            return;
+        }
+        // written before S of tile i - 2, whose norms this slot's neighbours hold
+        S.norms[i & 3][key] = norm;
+        uint8_t *dst = k_smem + buf * C::TileBytes + key * 128;
+#pragma unroll
+        for (int e = 0; e < D / 8; ++e) {
+            constexpr uint32_t kMask = B == 4 ? 0xffffffffu : (1u << (8 * B)) - 1u;
+            const int bit = e * 8 * B, at = bit >> 5, sh = bit & 31;
+            const uint32_t w = (sh == 0 ? row[at] : __funnelshift_r(row[at], row[at + 1], sh)) & kMask;
+            *reinterpret_cast<uint4 *>(dst + (e >> 3) * kTile * 128 + (((e & 7) ^ (key & 7)) << 4)) =
+                centroids<B>(nibbles<B>(w), lo, hi);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(smem_u32(&S.k_full[buf]));
+            mbar_arrive(smem_u32(&S.n_full[i & 3]));
+        }
+    }
+}
+
+template <int D, bool kBF16>
+__device__ void mma_role(const Params &p, Book &B, uint8_t *v_ptr, uint32_t k_smem, uint32_t v_smem, uint32_t tmem)
+{
+    using C = Cfg<D>;
+    constexpr uint32_t kFmt = kBF16 ? kFmtBF16 : kFmtF16;
+    constexpr uint32_t kIdS = idesc(kAccF32, kFmtF16, kFmtF16, kQueries, kTile);
+    constexpr uint32_t kIdO = idesc(kAccF32, kFmt, kFmt, kQueries, D) | kBMajorMN;
+    const int lane = threadIdx.x & 31;
+    Cursor sc(p.w, B), pv(p.w, B);
+    uint32_t i = 0, runs = 0;                                  // tiles and runs scored
+    auto wait = [&](uint64_t &bar, uint32_t parity, unsigned what) {
+        if (mbar_wait_warp(smem_u32(&bar), parity)) return true;
+        if (lane == 0) atomicOr(&g_status, what);
+        return false;
+    };
+    auto score = [&] {
+        if (!sc.more) return true;
+        const int buf = i & 1;
+        if (sc.k == 0 && !wait(B.q_full, runs++ & 1, kErrTimeoutDrain)) return false;
+        if (!wait(B.k_full[buf], (i >> 1) & 1, kErrTimeoutLoad)) return false;
+        tc_fence_after_sync();
+        if (elect_one()) {
+            const uint32_t kb = k_smem + buf * C::TileBytes;
+#pragma unroll
+            for (int part = 0; part < 2; ++part)               // the queries' high, then low parts
+#pragma unroll
+                for (int e = 0; e < D / 16; ++e)
+                    mma_f16_ts(tmem + buf * kTile, tmem + C::QCol + part * (D / 2) + e * 8,
+                               desc_k_sw128(kb + (e >> 2) * kTile * 128 + (e & 3) * 32), kIdS, part + e > 0);
+            mma_commit(smem_u32(&B.k_empty[buf]));
+            mma_commit(smem_u32(&B.s_full[buf]));
+        }
+        ++i;
+        sc.next();
+        return true;
+    };
+    bool ok = score() && score();
+    for (uint32_t j = 0; ok && pv.more; ++j) {
+        const int buf = j & 1, s = j % C::VStages;
+        if (!wait(B.p_full[buf], (j >> 1) & 1, kErrTimeoutDrain)) break;
+        if (!wait(B.v_full[s], (j / C::VStages) & 1, kErrTimeoutLoad)) break;
+        const int keys = pv.keys();
+        if (pv.r.seq >= 0 && keys < kTile) {
+            for (int e = 0; e < C::Blocks; ++e) {
+                uint4 *rows = reinterpret_cast<uint4 *>(v_ptr + s * C::TileBytes + e * kTile * 128);
+                for (int y = keys * 8 + lane; y < kTile * 8; y += 32) rows[y] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+        }
+        tc_fence_after_sync();
+        if (elect_one()) {
+#pragma unroll
+            for (int e = 0; e < kTile / 16; ++e)
+                mma_f16_ts(tmem + C::OCol, tmem + buf * kTile + e * 8,
+                           desc_mn_sw128(v_smem + s * C::TileBytes + e * 2048, kTile * 128), kIdO, pv.k > 0 || e > 0);
+            mma_commit(smem_u32(&B.v_empty[s]));
+            mma_commit(smem_u32(&B.o_done));
+        }
+        pv.next();
+        ok = score();
+    }
+    // all products complete before the tensor memory is freed
+    if (elect_one()) mma_commit(smem_u32(&B.drain));
+    __syncwarp();
+    mbar_wait_warp(smem_u32(&B.drain), 0);
+}
+
+template <int D>
+__device__ void tma_role(const Params &p, Book &B, uint32_t v_smem)
+{
+    using C = Cfg<D>;
+    if ((threadIdx.x & 31) != 0) return;
+    uint32_t j = 0;
+    for (Cursor c(p.w, B); c.more; c.next(), ++j) {
+        const int s = j % C::VStages;
+        if (!mbar_wait(smem_u32(&B.v_empty[s]), ((j / C::VStages) & 1) ^ 1)) {
+            atomicOr(&g_status, kErrTimeoutMma);
+            break;
+        }
+        const uint32_t bar = smem_u32(&B.v_full[s]);
+        mbar_arrive_expect_tx(bar, C::TileBytes);
+        const int z = c.r.seq >= 0 ? static_cast<int>(c.r.seg) : c.r.head;
+        for (int e = 0; e < C::Blocks; ++e)
+            tma_load_3d(v_smem + s * C::TileBytes + e * kTile * 128, c.r.seq >= 0 ? &p.own_v : &p.prefix_v, e * 64,
+                        c.tile() * kTile, z, bar);
+    }
+    for (uint32_t k = 0; k < C::VStages && k < j; ++k)         // every load lands before the CTA exits
+        mbar_wait(smem_u32(&B.v_full[(j - 1 - k) % C::VStages]), ((j - 1 - k) / C::VStages) & 1);
+}
+
+template <int D, int NB, bool kBF16>
+__global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_constant__ Params p)
+{
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Book B;
+    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t *v_ptr = smem + C::KStages * C::TileBytes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == kWarpTma && lane == 0) {
+        for (int s = 0; s < C::VStages; ++s) {
+            mbar_init(smem_u32(&B.v_full[s]), 1);
+            mbar_init(smem_u32(&B.v_empty[s]), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&B.k_full[s]), 4);
+            mbar_init(smem_u32(&B.k_empty[s]), 1);
+            mbar_init(smem_u32(&B.s_full[s]), 1);
+            mbar_init(smem_u32(&B.p_full[s]), 4);
+        }
+        for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&B.n_full[s]), 4);
+        mbar_init(smem_u32(&B.q_full), 4);
+        mbar_init(smem_u32(&B.o_done), 1);
+        mbar_init(smem_u32(&B.drain), 1);
+        fence_mbar_init();
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(smem_u32(&B.tmem_base), 512);
+        tmem_relinquish();
+    }
+    if (p.w.batch <= kIndexed)
+        for (int b = threadIdx.x; b <= p.w.batch; b += kThreads) {
+            B.start[b] = shared::own_start(p.w, b);
+            if (b < p.w.batch) B.len[b] = shared::length(p.w, b);
+        }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = B.tmem_base;
+    if (warp < 4) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        softmax_role<D, kBF16>(p, B, tmem);
+    } else if (warp < 8) {
+        code_role<D, NB>(p, B, smem);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kWarpMma) mma_role<D, kBF16>(p, B, v_ptr, smem_u32(smem), smem_u32(v_ptr), tmem);
+        else if (warp == kWarpTma) tma_role<D>(p, B, smem_u32(v_ptr));
+    }
+    __syncwarp();
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+}
+
+// (heads, rows, d) dense values, box of 64 elements x 128 rows
+bool make_map(CUtensorMap *map, const void *base, int dtype, int d, int64_t rows, int64_t heads)
+{
+    if (rows == 0) return true;                                // never loaded from
+    const EncodeTiledFn encode = encode_tiled();
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(heads)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(d) * 2 * rows};
+    const cuuint32_t box[3] = {64, kTile, 1}, es[3] = {1, 1, 1};
+    return encode(map, dtype == AXR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                  const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// half_codebook of (d, b), kept
+HalfCodebook codebook_of(const Codebook &cb)
+{
+    static std::mutex mu;
+    static HalfCodebook kept[2][kMaxBits + 1];
+    static bool have[2][kMaxBits + 1];
+    std::lock_guard<std::mutex> lock(mu);
+    const int x = cb.d == 128;
+    if (!have[x][cb.b]) {
+        kept[x][cb.b] = half_codebook(cb.centroids, cb.d, cb.b);
+        have[x][cb.b] = true;
+    }
+    return kept[x][cb.b];
+}
+
+template <int D, int B, bool kBF16>
+cudaError_t launch(const Params &p, cudaStream_t stream)
+{
+    static std::atomic<unsigned long long> done{0};
+    const auto kernel = shared_tc_kernel<D, B, kBF16>;
+    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), smem_bytes<D>(), done);
+    if (e != cudaSuccess) return e;
+    kernel<<<p.w.ctas, kThreads, smem_bytes<D>(), stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <int D, bool kBF16>
+cudaError_t launch_b(const Params &p, int b, cudaStream_t stream)
+{
+    switch (b) {
+    case 1: return launch<D, 1, kBF16>(p, stream);
+    case 2: return launch<D, 2, kBF16>(p, stream);
+    case 3: return launch<D, 3, kBF16>(p, stream);
+    default: return launch<D, 4, kBF16>(p, stream);
+    }
+}
+
+}  // namespace
+
+bool shared_tc_supported(const SharedArgs &a)
+{
+    return a.vdtype != AXR_F32 && (a.d == 64 || a.d == 128) && encode_tiled();
+}
+
+Work shared_tc_work(int batch, int heads, int group, int d)
+{
+    Work w{};
+    w.batch = batch;
+    w.heads = heads;
+    w.group = group;
+    w.d = d;
+    w.bm = kQueries;
+    const int rows = batch * group;
+    w.row_tiles = (rows + w.bm - 1) / w.bm;
+    w.slot_rows = rows < w.bm ? rows : w.bm;
+    w.ctas = device_sm_count();
+    w.min_tiles = 1;
+    return w;
+}
+
+cudaError_t launch_shared_main_tc(const SharedArgs &a, const Work &w, cudaStream_t stream)
+{
+    Params p{};
+    if (!make_map(&p.prefix_v, a.prefix_V, a.vdtype, a.d, a.n, a.heads) ||
+        !make_map(&p.own_v, a.V, a.vdtype, a.d, a.capacity, static_cast<int64_t>(a.batch) * a.heads))
+        return cudaErrorInvalidValue;
+    p.w = w;
+    p.prefix_idx = a.prefix_idx;
+    p.idx = a.idx;
+    p.prefix_norms = a.prefix_norms;
+    p.norms = a.norms;
+    const HalfCodebook hc = codebook_of(a.cb);
+    p.inv_scale = 1.0f / hc.scale;
+    const int first = a.b == 4 ? 8 : 0, count = a.b == 4 ? 8 : 1 << a.b;
+    for (int i = 0; i < count; ++i) {
+        p.lo[i / 4] |= static_cast<uint32_t>(hc.bits[first + i] & 0xff) << (8 * (i % 4));
+        p.hi[i / 4] |= static_cast<uint32_t>(hc.bits[first + i] >> 8) << (8 * (i % 4));
+    }
+    AXR_DEBUG_ONLY(const uint64_t rows = static_cast<uint64_t>(a.heads) * a.n, pb = a.d * a.b / 8;
+                   const uint64_t own = static_cast<uint64_t>(a.batch) * a.heads * a.capacity;
+                   p.sp_prefix_idx = dbg::span(a.prefix_idx, rows * pb); p.sp_prefix_norms = dbg::span(a.prefix_norms, rows * 4);
+                   p.sp_idx = dbg::span(a.idx, own * pb); p.sp_norms = dbg::span(a.norms, own * 4);)
+    const bool bf16 = a.vdtype == AXR_BF16;
+    if (a.d == 64) return bf16 ? launch_b<64, true>(p, a.b, stream) : launch_b<64, false>(p, a.b, stream);
+    return bf16 ? launch_b<128, true>(p, a.b, stream) : launch_b<128, false>(p, a.b, stream);
+}
+
+unsigned int shared_tc_status(bool clear)
+{
+    unsigned int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_status, sizeof(v)) != cudaSuccess) return ~0u;
+    if (clear && v) {
+        const unsigned int z = 0;
+        cudaMemcpyToSymbol(g_status, &z, sizeof(z));
+    }
+    return v;
+}
+
+}  // namespace axr

@@ -135,6 +135,24 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity)
     return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
 }
 
+// The same wait on the critical path of a pipeline: try_wait as it comes, without
+// the long suspension, whose end costs more time than the wait.
+__device__ __forceinline__ bool mbar_wait_warp_fast(uint32_t bar, uint32_t parity)
+{
+    bool ok = true;
+    unsigned long long t0 = 0;
+    for (uint32_t i = 0; !mbar_try_wait(bar, parity); ++i) {
+        if ((i & 63u) != 63u) continue;
+        const unsigned long long t = globaltimer();
+        if (t0 == 0) t0 = t;
+        else if (t - t0 > kWaitNs) {
+            ok = false;
+            break;
+        }
+    }
+    return __all_sync(0xffffffffu, ok) != 0;
+}
+
 // 2-D tiled TMA load of one box into shared memory, completing on `bar`.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
 {
@@ -204,6 +222,21 @@ __device__ __forceinline__ void tc_fence_before_sync()
 __device__ __forceinline__ void tc_fence_after_sync()
 {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+// True in one lane of a whole, converged warp (the same one every time), which
+// then issues the warp's products and commits.  The compiler knows the branch to
+// hold one thread and keeps the operands in uniform registers; behind a test of
+// the lane number it does not.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
 }
 
 // D[tmem] (+)= A[smem desc] * B[smem desc]^T, kind::f16 (fp16/bf16 in, fp32 acc)
