@@ -12,7 +12,6 @@
 // makes the rescale rare enough for the softmax warps to do it themselves.
 //
 // A persistent CTA per SM with one TMA warp, one MMA warp and a softmax
-// warpgroup per query tile in flight:
 //   d <= 128: two query tiles (256 queries).  Their S take turns: while the tensor
 //     cores run one tile's products, the other tile's warps are in their softmax.
 //   d = 256: one query tile (O takes half of tensor memory) with two S buffers;
@@ -43,6 +42,7 @@ using namespace softmax;
 
 constexpr int kTile = 128;                     // queries of a tile, keys of a tile
 constexpr int kMaxStages = 12;
+constexpr int kPolyShare = 3;                  // of 8 pairs of exponentials on the FMA pipes
 
 __device__ unsigned int g_status;
 
@@ -56,7 +56,7 @@ struct Cfg {
     static constexpr int PieceBytes = kTile * D * 2 / Pieces;
     static constexpr int VKeys = kTile / Pieces;               // keys of a V piece
     static constexpr int Stages = D == 64 ? 11 : 5;
-    static constexpr int SoftmaxWarps = 4 * NQ;
+    static constexpr int SoftmaxWarps = 8 * NQ;                // two warps per 32 queries: one half of the keys each
     static constexpr int WarpMma = SoftmaxWarps, WarpTma = SoftmaxWarps + 1;
     static constexpr int Threads = (SoftmaxWarps + 2) * 32;
     static constexpr int OCol = 2 * kTile;                     // S buffers first, then O
@@ -68,14 +68,16 @@ struct Book {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2];        // S of a buffer is complete
-    uint64_t p_full[2][2];     // the first and second half of its P is written (and O rescaled where needed)
+    uint64_t p_full[2];        // its P is written (and O rescaled where needed)
     uint64_t o_done[2];        // a query tile's latest P V is complete
+    uint64_t tail;             // a V tile that reaches behind its sequence has landed
     uint64_t drain;
     uint32_t tmem_base;
+    float word[2][2][kTile];   // by query tile (one tile: by turn) and half: what those warps exchange
 };
 
 template <int D>
-constexpr size_t smem_bytes() { return 1024 + Cfg<D>::NQ * Cfg<D>::QBytes + Cfg<D>::Stages * Cfg<D>::PieceBytes + sizeof(Book); }
+constexpr size_t smem_bytes() { return Cfg<D>::NQ * Cfg<D>::QBytes + Cfg<D>::Stages * Cfg<D>::PieceBytes + sizeof(Book); }
 static_assert(smem_bytes<64>() <= 232448 && smem_bytes<128>() <= 232448 && smem_bytes<256>() <= 232448, "shared memory");
 
 struct Params {
@@ -116,59 +118,69 @@ __device__ __forceinline__ bool item_at(const Params &p, int64_t i, Item &x)
     return true;
 }
 
-// The softmax warpgroup of query tile t (buffer t; at NQ = 1 buffers 0 and 1 in
-// turn).  Thread = query.
+// Softmax of half `half` of every tile of keys for query tile t (buffer t; at
+// NQ = 1 buffers 0 and 1 in turn).  Thread = query.
 template <int D, bool kBF16>
-__device__ void softmax_role(const Params &p, Book &B, int t, uint32_t tmem)
+__device__ void softmax_role(const Params &p, Book &B, int t, int half, uint32_t tmem)
 {
     using C = Cfg<D>;
     const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+    const int r = warp * 32 + lane;                            // query of the tile
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t o_at = tmem + lanes + C::OCol + t * D;
+    const uint32_t o_at = tmem + lanes + C::OCol + t * D + half * (D / 2);   // this half's columns of O
     const int64_t items = static_cast<int64_t>(p.tiles) * p.s.heads * p.s.group;
+    const int meet_id = 1 + t * 4 + warp;
+    // a wait that runs out records a bit; the role then goes on without waiting, to
+    // keep meeting its partner
+    bool ok = true;
+    auto wait = [&](uint64_t &bar, uint32_t parity, unsigned what) {
+        if (ok && !mbar_wait_warp_fast(smem_u32(&bar), parity)) {
+            ok = false;
+            if (lane == 0) atomicOr(&g_status, what);
+        }
+    };
     uint32_t count = 0;                                        // tiles so far: phases of s_full and o_done
     for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
         Item x;
         if (!item_at<D>(p, i, x)) break;
         const int rows = t == 0 ? x.rows[0] : x.rows[1], n = t == 0 ? x.n[0] : x.n[1];
-        const bool idle = warp * 32 >= rows;                   // no query of this warp
-        const int first = x.t.row + t * kTile + warp * 32;     // the warp's first query
+        const bool idle = warp * 32 >= rows;                   // no query of these warps
+        const int first = x.t.row + t * kTile + warp * 32;     // the warps' first query
         const int past = x.t.len_k - x.t.len_q;
         float m = -INFINITY, l = 0.0f;
         for (int j = 0; j < n; ++j, ++count) {
             const int buf = C::NQ == 2 ? t : count & 1;
-            if (!mbar_wait_warp_fast(smem_u32(&B.s_full[buf]), (C::NQ == 2 ? count : count >> 1) & 1)) {
-                if (lane == 0) atomicOr(&g_status, kErrTimeoutMma);
-                return;
-            }
+            wait(B.s_full[buf], (C::NQ == 2 ? count : count >> 1) & 1, kErrTimeoutMma);
             if (!idle) {
                 tc_fence_after_sync();
                 const uint32_t s_at = tmem + lanes + buf * kTile;
-                const int seen = first + past + 1 - j * kTile; // keys of the tile that the warp's first query sees
-                const int lim = seen < kTile ? seen + lane : kTile;
+                const uint32_t s_half = s_at + 64 * half;      // this half's scores
+                const int seen = first + past + 1 - j * kTile; // keys of the tile that the warps' first query sees
+                const int lim = seen + lane - 64 * half;       // of this half that this query sees
                 float mx = -INFINITY;
-#pragma unroll 1
-                for (int c = 0; c < kTile; c += 32) {
+#pragma unroll
+                for (int c = 0; c < 64; c += 32) {
                     uint32_t s[32];
-                    tmem_ld32(s_at + c, s);
+                    tmem_ld32(s_half + c, s);
                     if (seen < kTile) mask32(s, lim - c);
                     mx = max32(s, mx);
                 }
+                float(*word)[kTile] = B.word[C::NQ == 2 ? t : count & 1];
+                word[half][r] = mx;
+                meet_partner(meet_id);
+                mx = fmaxf(mx, word[half ^ 1][r]);
                 if (j == 0) {
                     m = mx;
                 } else if (__any_sync(0xffffffffu, (mx - m) * p.scale > kLazy)) {
-                    // the last P V must be complete before O is rescaled
-                    if (!mbar_wait_warp(smem_u32(&B.o_done[t]), (count - 1) & 1)) {
-                        if (lane == 0) atomicOr(&g_status, kErrTimeoutMma);
-                        return;
-                    }
+                    // both warps see the same maxima; the last P V must be complete before O is rescaled
+                    wait(B.o_done[t], (count - 1) & 1, kErrTimeoutMma);
                     tc_fence_after_sync();
                     const float up = fmaxf(m, mx);
                     const float f = m == -INFINITY ? 0.0f : ex2((m - up) * p.scale);
                     m = up;
                     l *= f;
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
+                    for (int c = 0; c < D / 2; c += 32) {
                         uint32_t o[32];
                         tmem_ld32(o_at + c, o);
 #pragma unroll
@@ -180,44 +192,45 @@ __device__ void softmax_role(const Params &p, Book &B, int t, uint32_t tmem)
                 const float c0 = m == -INFINITY ? 0.0f : kBias<kBF16> - m * p.scale;
                 const uint64_t scale2 = pair(p.scale, p.scale), c2 = pair(c0, c0);
                 uint64_t sum0 = pair(l, 0.0f), sum1 = pair(0.0f, 0.0f);
-#pragma unroll 1
-                for (int c = 0; c < kTile; c += 32) {
+#pragma unroll
+                for (int c = 0; c < 64; c += 32) {
                     uint32_t s[32], w[16];
-                    tmem_ld32(s_at + c, s);
+                    tmem_ld32(s_half + c, s);
                     if (seen < kTile) mask32(s, lim - c);
-                    weights32<kBF16>(s, scale2, c2, sum0, sum1, w);
-                    tmem_st16(s_at + c / 2, w);                // over scores that are read already
-                    if ((c & 32) == 0) continue;
-                    // half by half, so that the products of the first run under the second
-                    tmem_wait_st();
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&B.p_full[buf][c >> 6]));
+                    weights32<kBF16, kPolyShare>(s, scale2, c2, sum0, sum1, w);
+                    tmem_st16(s_half + c / 2, w);              // over scores that are read already
                 }
                 float s0, s1, s2, s3;
                 unpair(sum0, s0, s1);
                 unpair(sum1, s2, s3);
                 l = (s0 + s1) + (s2 + s3);
-            } else if (lane == 0) {
-                mbar_arrive(smem_u32(&B.p_full[buf][0]));
-                mbar_arrive(smem_u32(&B.p_full[buf][1]));
+                tmem_wait_st();
+                tc_fence_before_sync();
+                // A wait tells a phase only from its neighbours.  With two S buffers the
+                // last two P V could both be running, or both be complete, at the wait
+                // below: see the last but one complete before the last can start.
+                if (C::NQ == 1 && j > 0 && j + 1 == n) wait(B.o_done[t], (count - 1) & 1, kErrTimeoutMma);
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&B.p_full[buf]));
         }
-        // the last two P V in turn: with two S buffers both may still be running, and a
-        // wait tells a phase only from its neighbours
-        for (int k = n < 2 ? n : 2; k > 0; --k)
-            if (!mbar_wait_warp(smem_u32(&B.o_done[t]), (count - k) & 1)) {
-                if (lane == 0) atomicOr(&g_status, kErrTimeoutMma);
-                return;
-            }
         if (idle) continue;
+        if (n > 0) wait(B.o_done[t], (count - 1) & 1, kErrTimeoutMma);
         tc_fence_after_sync();
-        const int r = warp * 32 + lane;
+        if (n > 0) {                                           // the other half's sum
+            float(*word)[kTile] = B.word[C::NQ == 2 ? t : count & 1];
+            word[half][r] = l;
+            meet_partner(meet_id);
+            l += word[half ^ 1][r];
+            // nobody writes the words again before both have read them
+            meet_partner(meet_id);
+        }
+        if (m == -INFINITY && l == l) l = 0.0f;                // no key: masked weights are 2^-126, not 0
         const int64_t at = x.t.first_q + x.t.row + t * kTile + r;
         const float inv = l > 0.0f ? 1.0f / l : l;             // 0 for no key, NaN stays NaN
-        char *dst = static_cast<char *>(p.out) + (x.hq * p.s.o_head + at * p.s.o_row) * 2;
+        char *dst = static_cast<char *>(p.out) + (x.hq * p.s.o_head + at * p.s.o_row + half * (D / 2)) * 2;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = 0; c < D / 2; c += 32) {
             uint32_t o[32];
             if (n > 0) {
                 tmem_ld32(o_at + c, o);
@@ -238,7 +251,7 @@ __device__ void softmax_role(const Params &p, Book &B, int t, uint32_t tmem)
                 }
             }
         }
-        if (p.lse && r < rows) {
+        if (p.lse && half == 0 && r < rows) {
             float *to = p.lse + static_cast<int64_t>(x.hq) * p.s.total_q + at;
             const float base = m == -INFINITY ? -INFINITY : m * p.scale - kBias<kBF16>;
             if (AXR_IN(p.sp_lse, to, 4)) *to = (base + log2f(l)) * kLn2;
@@ -248,24 +261,21 @@ __device__ void softmax_role(const Params &p, Book &B, int t, uint32_t tmem)
 }
 
 template <int D>
-__device__ void tma_role(const Params &p, Book &B, uint32_t q_smem, uint32_t ring)
+__device__ void tma_role(const Params &p, Book &B, uint8_t *ring_ptr, uint32_t q_smem, uint32_t ring)
 {
     using C = Cfg<D>;
     const int lane = threadIdx.x & 31;
     const int64_t items = static_cast<int64_t>(p.tiles) * p.s.heads * p.s.group;
-    uint32_t pieces = 0, q_count[2] = {0, 0};
+    uint32_t pieces = 0, tails = 0, q_count[2] = {0, 0};
     bool ok = true;
-    // the next stage of the ring, free; its barrier expects a piece
-    auto next = [&](uint32_t &dst, uint32_t &bar) {
-        const int s = pieces % C::Stages;
+    // the next stage of the ring, once it is free
+    auto next = [&](uint32_t &s) {
+        s = pieces % C::Stages;
         if (!mbar_wait(smem_u32(&B.empty[s]), ((pieces / C::Stages) & 1) ^ 1)) {
             atomicOr(&g_status, kErrTimeoutMma);
             return false;
         }
         ++pieces;
-        dst = ring + s * C::PieceBytes;
-        bar = smem_u32(&B.full[s]);
-        mbar_arrive_expect_tx(bar, C::PieceBytes);
         return true;
     };
     for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
@@ -289,21 +299,27 @@ __device__ void tma_role(const Params &p, Book &B, uint32_t q_smem, uint32_t rin
             };
             auto load_k = [&](int j) {
                 for (int c = 0; c < C::Pieces; ++c) {
-                    uint32_t dst, bar;
-                    if (!next(dst, bar)) return false;
+                    uint32_t s;
+                    if (!next(s)) return false;
+                    const uint32_t bar = smem_u32(&B.full[s]);
+                    mbar_arrive_expect_tx(bar, C::PieceBytes);
                     for (int e = 0; e < C::QBlocks / C::Pieces; ++e)
-                        tma_load_3d(dst + e * kTile * 128, &p.k, (c * (C::QBlocks / C::Pieces) + e) * 64,
-                                    x.t.first_k + j * kTile, h, bar);
+                        tma_load_3d(ring + s * C::PieceBytes + e * kTile * 128, &p.k,
+                                    (c * (C::QBlocks / C::Pieces) + e) * 64, x.t.first_k + j * kTile, h, bar);
                 }
                 return true;
             };
             auto load_v = [&](int j) {
+                const bool tail = x.t.len_k < (j + 1) * kTile;
+                if (tail) mbar_arrive_expect_tx(smem_u32(&B.tail), C::Pieces * C::PieceBytes);
                 for (int c = 0; c < C::Pieces; ++c) {
-                    uint32_t dst, bar;
-                    if (!next(dst, bar)) return false;
+                    uint32_t s;
+                    if (!next(s)) return false;
+                    const uint32_t bar = smem_u32(tail ? &B.tail : &B.full[s]);
+                    if (!tail) mbar_arrive_expect_tx(bar, C::PieceBytes);
                     for (int e = 0; e < C::QBlocks; ++e)
-                        tma_load_3d(dst + e * C::VKeys * 128, &p.v, e * 64, x.t.first_k + j * kTile + c * C::VKeys, h,
-                                    bar);
+                        tma_load_3d(ring + s * C::PieceBytes + e * C::VKeys * 128, &p.v, e * 64,
+                                    x.t.first_k + j * kTile + c * C::VKeys, h, bar);
                 }
                 return true;
             };
@@ -318,6 +334,27 @@ __device__ void tma_role(const Params &p, Book &B, uint32_t q_smem, uint32_t rin
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
+        // The last V tile's rows behind the sequence are weighed with 0: clear them, lest
+        // they hold NaN, before the tile is announced.  No tile is loaded after it.
+        pieces = __shfl_sync(0xffffffffu, pieces, 0);
+        const int keys = x.t.len_k - (x.most - 1) * kTile;
+        if (x.most > 0 && keys < kTile) {
+            if (!mbar_wait_warp_fast(smem_u32(&B.tail), tails++ & 1)) {
+                if (lane == 0) atomicOr(&g_status, kErrTimeoutLoad);
+                break;
+            }
+            for (int c = 0; c < C::Pieces; ++c) {
+                const uint32_t s = (pieces - C::Pieces + c) % C::Stages;
+                const int from = max(keys - c * C::VKeys, 0);
+                for (int e = 0; e < C::QBlocks; ++e) {
+                    uint4 *rows = reinterpret_cast<uint4 *>(ring_ptr + s * C::PieceBytes + e * C::VKeys * 128);
+                    for (int y = from * 8 + lane; y < C::VKeys * 8; y += 32) rows[y] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&B.full[s]));
+            }
+        }
     }
     if (lane == 0) {                                           // every load lands before the CTA exits
         for (uint32_t k = 0; k < C::Stages && k < pieces; ++k) {
@@ -329,135 +366,180 @@ __device__ void tma_role(const Params &p, Book &B, uint32_t q_smem, uint32_t rin
     }
 }
 
+// column in its S buffer of the weights of a tile's key k: each half of the tile has
+// them where its own scores were
+__host__ __device__ constexpr int weights_at(int k) { return (k & 64) + (k & 63) / 2; }
+
+// A position in the ring of pieces.
+template <int D>
+struct RingAt {
+    uint32_t stage = 0, phase = 0;
+    __device__ __forceinline__ void step()
+    {
+        if (++stage == Cfg<D>::Stages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// The products of an item, issued by one thread: a warp's votes and reconvergences
+// between the steps, queued behind the softmax warps' instructions, took longer
+// than the products.
 template <int D, bool kBF16>
-__device__ void mma_role(const Params &p, Book &B, uint8_t *ring_ptr, uint32_t q_smem, uint32_t ring, uint32_t tmem)
+struct Products {
+    using C = Cfg<D>;
+    static constexpr uint32_t kFmt = kBF16 ? kFmtBF16 : kFmtF16;
+    static constexpr uint32_t kIdS = idesc(kAccF32, kFmt, kFmt, kTile, kTile);
+    static constexpr uint32_t kIdO = idesc(kAccF32, kFmt, kFmt, kTile, D) | kBMajorMN;
+    static constexpr uint32_t kPiece = C::PieceBytes >> 4;     // in a descriptor's units
+    Book &B;
+    const uint64_t q_desc, k_desc, v_desc;                     // of query tile 0 and ring stage 0
+    const uint32_t tmem;
+    RingAt<D> at;                                              // the next piece
+    uint32_t q_phase = 0, p_phase[2] = {0, 0};
+    uint32_t tiles = 0;                                        // d = 256: tiles so far (S buffers in turn)
+
+    __device__ Products(Book &book, uint32_t q_smem, uint32_t ring, uint32_t tm)
+        : B(book), q_desc(desc_k_sw128(q_smem)), k_desc(desc_k_sw128(ring)),
+          v_desc(desc_mn_sw128(ring, C::VKeys * 128)), tmem(tm)
+    {
+    }
+    __device__ __forceinline__ bool wait(uint64_t &bar, uint32_t parity, unsigned what)
+    {
+        if (mbar_wait_fast(smem_u32(&bar), parity)) return true;
+        atomicOr(&g_status, what);
+        return false;
+    }
+    __device__ __forceinline__ bool piece(const RingAt<D> &r) { return wait(B.full[r.stage], r.phase, kErrTimeoutLoad); }
+    // S of `buf` = query tile t times the K tile at r
+    __device__ __forceinline__ bool score(int t, int buf, RingAt<D> r, bool last)
+    {
+        constexpr int kBlocks = C::QBlocks / C::Pieces;
+#pragma unroll
+        for (int c = 0; c < C::Pieces; ++c) {
+            if (!piece(r)) return false;
+            tc_fence_after_sync();
+            const uint64_t qd = q_desc + ((t * C::QBytes + c * kBlocks * kTile * 128) >> 4), kd = k_desc + r.stage * kPiece;
+#pragma unroll
+            for (int e = 0; e < kBlocks * 4; ++e) {
+                const uint32_t off = ((e >> 2) * kTile * 128 + (e & 3) * 32) >> 4;
+                mma_f16_ss(tmem + buf * kTile, qd + off, kd + off, kIdS, c + e > 0);
+            }
+            if (last) mma_commit(smem_u32(&B.empty[r.stage]));
+            r.step();
+        }
+        mma_commit(smem_u32(&B.s_full[buf]));
+        return true;
+    }
+    // O of query tile t (+)= P of `buf` times the V tile at r
+    __device__ __forceinline__ bool weigh(int t, int buf, RingAt<D> r, bool first, bool last)
+    {
+        if (!piece(r) || !wait(B.p_full[buf], p_phase[buf], kErrTimeoutDrain)) return false;
+        p_phase[buf] ^= 1;
+#pragma unroll
+        for (int c = 0; c < C::Pieces; ++c) {
+            if (c > 0 && !piece(r)) return false;
+            tc_fence_after_sync();
+            const uint64_t vd = v_desc + r.stage * kPiece;
+#pragma unroll
+            for (int e = 0; e < C::VKeys / 16; ++e)
+                mma_f16_ts(tmem + C::OCol + t * D, tmem + buf * kTile + weights_at(c * C::VKeys + e * 16),
+                           vd + (e * 2048 >> 4), kIdO, !first || c + e > 0);
+            if (last) mma_commit(smem_u32(&B.empty[r.stage]));
+            r.step();
+        }
+        mma_commit(smem_u32(&B.o_done[t]));
+        return true;
+    }
+    __device__ __forceinline__ void skip_tile()
+    {
+#pragma unroll
+        for (int c = 0; c < C::Pieces; ++c) at.step();
+    }
+    __device__ __forceinline__ bool wait_q(int t)
+    {
+        const bool ok = wait(B.q_full[t], (q_phase >> t) & 1, kErrTimeoutLoad);
+        q_phase ^= 1u << t;
+        return ok;
+    }
+    __device__ __forceinline__ void free_q(int t) { mma_commit(smem_u32(&B.q_empty[t])); }
+
+    // two query tiles with n0 and n1 tiles of keys; n: the larger; pieces come as
+    // K0 V0 K1 V1 ...; a tile is last used by query tile 1 unless that one is empty
+    __device__ bool item2(int n0, int n1, int n)
+    {
+        const bool two = n1 > 0;
+        bool ok = true;
+        if (n0 > 0) {
+            ok = wait_q(0) && score(0, 0, at, !two);
+            if (n0 == 1) free_q(0);
+        }
+        if (two && ok) {
+            ok = wait_q(1) && score(1, 1, at, true);
+            if (n1 == 1) free_q(1);
+        }
+        if (n > 0) skip_tile();                                // K0
+        for (int j = 0; ok && j < n; ++j) {
+            const RingAt<D> v = at;
+            skip_tile();
+            const RingAt<D> k = at;
+            if (j + 1 < n) skip_tile();
+            if (j < n0) {
+                ok = weigh(0, 0, v, j == 0, !two);
+                if (ok && j + 1 < n0) {
+                    ok = score(0, 0, k, !two);
+                    if (j + 2 == n0) free_q(0);
+                }
+            }
+            if (ok && j < n1) {
+                ok = weigh(1, 1, v, j == 0, true);
+                if (ok && j + 1 < n1) {
+                    ok = score(1, 1, k, true);
+                    if (j + 2 == n1) free_q(1);
+                }
+            }
+        }
+        return ok;
+    }
+    // one query tile with n tiles of keys; pieces come as K0 K1 V0 K2 V1 K3 ...
+    __device__ bool item1(int n)
+    {
+        if (n == 0) return true;
+        bool ok = wait_q(0) && score(0, tiles & 1, at, true);
+        skip_tile();
+        if (ok && n > 1) {
+            ok = score(0, (tiles + 1) & 1, at, true);
+            skip_tile();
+        }
+        if (n <= 2) free_q(0);
+        for (int j = 0; ok && j < n; ++j) {
+            const int buf = (tiles + j) & 1;
+            ok = weigh(0, buf, at, j == 0, true);
+            skip_tile();
+            if (ok && j + 2 < n) {
+                ok = score(0, buf, at, true);
+                skip_tile();
+                if (j + 3 == n) free_q(0);
+            }
+        }
+        tiles += n;
+        return ok;
+    }
+};
+
+template <int D, bool kBF16>
+__device__ void mma_role(const Params &p, Book &B, uint32_t q_smem, uint32_t ring, uint32_t tmem)
 {
     using C = Cfg<D>;
-    constexpr uint32_t kFmt = kBF16 ? kFmtBF16 : kFmtF16;
-    constexpr uint32_t kIdS = idesc(kAccF32, kFmt, kFmt, kTile, kTile);
-    constexpr uint32_t kIdO = idesc(kAccF32, kFmt, kFmt, kTile, D) | kBMajorMN;
-    const int lane = threadIdx.x & 31;
     const int64_t items = static_cast<int64_t>(p.tiles) * p.s.heads * p.s.group;
-    uint32_t pieces = 0, q_count[2] = {0, 0}, p_count[2] = {0, 0};   // indexed by constants only
-    bool ok = true;
-    auto wait = [&](uint64_t &bar, uint32_t parity, unsigned what) {
-        if (mbar_wait_warp_fast(smem_u32(&bar), parity)) return true;
-        if (lane == 0) atomicOr(&g_status, what);
-        return false;
-    };
-    auto wait_piece = [&](uint32_t k) { return wait(B.full[k % C::Stages], (k / C::Stages) & 1, kErrTimeoutLoad); };
-    auto release = [&](uint32_t k) {
-        if (elect_one()) mma_commit(smem_u32(&B.empty[k % C::Stages]));
-    };
-    // S of `buf` = query tile t times the K tile whose pieces start at k
-    auto score = [&](int t, int buf, uint32_t k, bool last) {
-        constexpr int kBlocks = C::QBlocks / C::Pieces;
-        for (int c = 0; c < C::Pieces; ++c) {
-            if (!wait_piece(k + c)) return false;
-            tc_fence_after_sync();
-            if (elect_one()) {
-                const uint32_t kb = ring + ((k + c) % C::Stages) * C::PieceBytes;
-                const uint32_t qb = q_smem + t * C::QBytes + c * kBlocks * kTile * 128;
-#pragma unroll
-                for (int e = 0; e < kBlocks * 4; ++e) {
-                    const uint32_t off = (e >> 2) * kTile * 128 + (e & 3) * 32;
-                    mma_f16_ss(tmem + buf * kTile, desc_k_sw128(qb + off), desc_k_sw128(kb + off), kIdS, c + e > 0);
-                }
-            }
-            if (last) release(k + c);
-        }
-        if (elect_one()) mma_commit(smem_u32(&B.s_full[buf]));
-        return true;
-    };
-    // O of query tile t (+)= P of `buf` times the V tile whose pieces start at k;
-    // phase: that of P; keys: the tile's keys that belong to the sequence; fresh: the
-    // tile's first use
-    auto weigh = [&](int t, int buf, uint32_t phase, uint32_t k, int keys, bool first, bool fresh, bool last) {
-        for (int c = 0; c < C::Pieces; ++c) {
-            if (!wait_piece(k + c)) return false;
-            const uint32_t off = ((k + c) % C::Stages) * C::PieceBytes;
-            if (fresh && keys < (c + 1) * C::VKeys) {
-                // rows behind the sequence are weighed with 0: clear them, lest they hold NaN
-                const int from = max(keys - c * C::VKeys, 0);
-                for (int e = 0; e < C::QBlocks; ++e) {
-                    uint4 *rows = reinterpret_cast<uint4 *>(ring_ptr + off + e * C::VKeys * 128);
-                    for (int y = from * 8 + lane; y < C::VKeys * 8; y += 32) rows[y] = make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-            }
-            constexpr int kHalves = 2 / C::Pieces;             // halves of P that the piece meets
-            for (int h = 0; h < kHalves; ++h) {
-                if (!wait(B.p_full[buf][c * kHalves + h], phase, kErrTimeoutDrain)) return false;
-                tc_fence_after_sync();
-                if (elect_one()) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mma_f16_ts(tmem + C::OCol + t * D, tmem + buf * kTile + ((c * kHalves + h) * 4 + e) * 8,
-                                   desc_mn_sw128(ring + off + (h * 4 + e) * 2048, C::VKeys * 128), kIdO,
-                                   !first || c + h + e > 0);
-                }
-            }
-            if (last) release(k + c);
-        }
-        if (elect_one()) mma_commit(smem_u32(&B.o_done[t]));
-        return true;
-    };
-    auto wait_q = [&](int t) {
-        if (!wait(B.q_full[t], q_count[t] & 1, kErrTimeoutLoad)) return false;
-        ++q_count[t];
-        return true;
-    };
-    auto free_q = [&](int t) {
-        if (elect_one()) mma_commit(smem_u32(&B.q_empty[t]));
-    };
-    for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-        Item x;
-        if (!item_at<D>(p, i, x)) break;
-        const int len = x.t.len_k;
-        if constexpr (C::NQ == 2) {
-            // pieces in order: K0, V0, K1, V1, ...; a tile is last used by query
-            // tile 1 unless that one has fewer tiles
-            const bool two = x.n[1] > 0;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (!ok || x.n[t] == 0) continue;
-                ok = wait_q(t) && score(t, t, pieces, t == 1 || !two);
-                if (x.n[t] == 1) free_q(t);
-            }
-            for (int j = 0; ok && j < x.most; ++j) {
-                const uint32_t v = pieces + 2 * j + 1, k = v + 1;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (!ok || j >= x.n[t]) continue;
-                    ok = weigh(t, t, p_count[t]++ & 1, v, len - j * kTile, j == 0, t == 0 || j >= x.n[0], t == 1 || !two);
-                    if (ok && j + 1 < x.n[t]) {
-                        ok = score(t, t, k, t == 1 || !two);
-                        if (j + 2 == x.n[t]) free_q(t);
-                    }
-                }
-            }
-            pieces += 2 * x.most;
-        } else {
-            // K0 K1 V0 K2 V1 ...: tile j's K is the (j < 2 ? j : 2 j - 1)-th tile of the
-            // ring, its V the one after K of tile j + 1
-            if (x.most == 0) continue;
-            const int n = x.most;
-            auto k_tile = [&](int j) { return pieces + C::Pieces * (j < 2 ? j : 2 * j - 1); };
-            auto v_tile = [&](int j) { return pieces + C::Pieces * (j + min(j + 2, n)); };
-            const uint32_t at = p_count[0];                    // S buffers in turn over all items
-            ok = wait_q(0) && score(0, at & 1, k_tile(0), true) && (n < 2 || score(0, (at + 1) & 1, k_tile(1), true));
-            if (n <= 2) free_q(0);
-            for (int j = 0; ok && j < n; ++j) {
-                ok = weigh(0, (at + j) & 1, ((at + j) >> 1) & 1, v_tile(j), len - j * kTile, j == 0, true, true);
-                if (ok && j + 2 < n) {
-                    ok = score(0, (at + j) & 1, k_tile(j + 2), true);
-                    if (j + 3 == n) free_q(0);
-                }
-            }
-            p_count[0] += n;
-            pieces += 2 * C::Pieces * n;
-        }
+    Products<D, kBF16> x(B, q_smem, ring, tmem);
+    for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+        Item it;
+        if (!item_at<D>(p, i, it)) break;
+        bool ok = true;
+        if (elect_one()) ok = C::NQ == 2 ? x.item2(it.n[0], it.n[1], it.most) : x.item1(it.most);
+        if (__any_sync(0xffffffffu, !ok)) break;
     }
     // all products complete before the tensor memory is freed
     if (elect_one()) mma_commit(smem_u32(&B.drain));
@@ -469,10 +551,13 @@ template <int D, bool kBF16>
 __global__ void __launch_bounds__(Cfg<D>::Threads, 1) prompt_tc_kernel(const __grid_constant__ Params p)
 {
     using C = Cfg<D>;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ Book B;
-    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    extern __shared__ __align__(1024) uint8_t smem[];          // query tiles, ring, bookkeeping
+    if ((smem_u32(smem) & 1023) != 0) {                        // the swizzled tiles need 1024-byte boundaries
+        if (threadIdx.x == 0) atomicOr(&g_status, kErrLayout);
+        return;
+    }
     uint8_t *ring_ptr = smem + C::NQ * C::QBytes;
+    Book &B = *reinterpret_cast<Book *>(ring_ptr + C::Stages * C::PieceBytes);
     const uint32_t q_smem = smem_u32(smem), ring = smem_u32(ring_ptr);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == C::WarpTma && lane == 0) {
@@ -484,10 +569,10 @@ __global__ void __launch_bounds__(Cfg<D>::Threads, 1) prompt_tc_kernel(const __g
             mbar_init(smem_u32(&B.q_full[t]), 1);
             mbar_init(smem_u32(&B.q_empty[t]), 1);
             mbar_init(smem_u32(&B.s_full[t]), 1);
-            mbar_init(smem_u32(&B.p_full[t][0]), 4);
-            mbar_init(smem_u32(&B.p_full[t][1]), 4);
+            mbar_init(smem_u32(&B.p_full[t]), 8);
             mbar_init(smem_u32(&B.o_done[t]), 1);
         }
+        mbar_init(smem_u32(&B.tail), 1);
         mbar_init(smem_u32(&B.drain), 1);
         fence_mbar_init();
         prefetch_tensormap(&p.q);
@@ -503,10 +588,10 @@ __global__ void __launch_bounds__(Cfg<D>::Threads, 1) prompt_tc_kernel(const __g
     tc_fence_after_sync();
     const uint32_t tmem = B.tmem_base;
     if (warp < C::SoftmaxWarps) {
-        softmax_role<D, kBF16>(p, B, warp >> 2, tmem);
+        softmax_role<D, kBF16>(p, B, warp >> 3, (warp >> 2) & 1, tmem);
     } else {
-        if (warp == C::WarpTma) tma_role<D>(p, B, q_smem, ring);
-        else if (warp == C::WarpMma) mma_role<D, kBF16>(p, B, ring_ptr, q_smem, ring, tmem);
+        if (warp == C::WarpTma) tma_role<D>(p, B, ring_ptr, q_smem, ring);
+        else if (warp == C::WarpMma) mma_role<D, kBF16>(p, B, q_smem, ring, tmem);
     }
     __syncwarp();
     tc_fence_before_sync();
@@ -537,13 +622,13 @@ cudaError_t launch(Params &p, const PromptArgs &a, cudaStream_t stream)
     using C = Cfg<D>;
     static std::atomic<unsigned long long> done{0};
     const auto kernel = prompt_tc_kernel<D, kBF16>;
-    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), smem_bytes<D>() - sizeof(Book), done);
+    cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), smem_bytes<D>(), done);
     if (e != cudaSuccess) return e;
     p.tiles = prompt_tiles(a.s, C::BM);
     p.scale = kLog2e / sqrtf(static_cast<float>(D));
     const int64_t items = static_cast<int64_t>(p.tiles) * a.s.heads * a.s.group;
     const int sms = device_sm_count();
-    kernel<<<items < sms ? static_cast<int>(items) : sms, C::Threads, smem_bytes<D>() - sizeof(Book), stream>>>(p);
+    kernel<<<items < sms ? static_cast<int>(items) : sms, C::Threads, smem_bytes<D>(), stream>>>(p);
     return cudaGetLastError();
 }
 

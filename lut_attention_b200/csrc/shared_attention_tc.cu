@@ -12,13 +12,14 @@
 // that only the centroids' rounding (at most 2^-13 relatively) is left in S.
 //
 // A persistent CTA per SM walks its stretch of tiles (shared.cuh) with
-//   warps 0-3   softmax: Q into tensor memory (an operand from there, which spares
-//               shared memory), the weights, and a run's end into its slot;
-//   warps 4-7   codes to centroids: thread = key, its packed row loaded one tile
-//               ahead, 16-byte stores in the swizzled rows the products read;
-//   warp 8      products: S of the tile after next is issued before P V of this one,
+//   warps 0-7   softmax: Q into tensor memory (an operand from there, which spares
+//               shared memory), the weights (two threads a query, softmax_tc.cuh),
+//               and a run's end into its slot;
+//   warps 8-15  codes to centroids: two threads a key, the packed rows loaded one
+//               tile ahead, 16-byte stores in the swizzled rows the products read;
+//   warp 16     products: S of the tile after next is issued before P V of this one,
 //               so the tensor cores run under the softmax;
-//   warp 9      TMA loads of V, a ring of tiles.
+//   warp 17     TMA loads of V, a ring of tiles.
 // Rows of V behind a sequence's length may hold anything; they are cleared in
 // shared memory, since 0 times NaN is NaN.
 //
@@ -47,11 +48,10 @@ using shared::Work;
 
 constexpr int kTile = shared::kTileKeys;
 constexpr int kQueries = 128;
-constexpr int kThreads = 384;                  // three warpgroups: softmax, codes, products and loads
-constexpr int kWarpMma = 8, kWarpTma = 9;
-// of the 168 registers a thread that 384 threads get at launch
-constexpr int kSoftmaxRegs = 232, kOtherRegs = 104;
-static_assert(kSoftmaxRegs + 168 + kOtherRegs <= 3 * 168, "registers of the block");
+constexpr int kCodeWarps = 8;                  // after the eight of the softmax
+constexpr int kWarpMma = 8 + kCodeWarps, kWarpTma = kWarpMma + 1;
+constexpr int kThreads = (kWarpTma + 1) * 32;
+constexpr int kPolyShare = 3;                  // of 8 pairs of exponentials on the FMA pipes
 constexpr int kIndexed = 1024;                 // sequences whose starts and lengths fit shared memory
 
 __device__ unsigned int g_status;
@@ -74,6 +74,7 @@ struct Book {
     uint64_t n_full[4];        // norms of a tile are written
     uint64_t q_full, o_done, drain;
     uint32_t tmem_base;
+    float word[2][2][kQueries];                                // by turn and half: what they exchange
     alignas(16) float norms[4][kTile];                         // read 16 bytes at a time
     int32_t start[kIndexed + 1], len[kIndexed];
 };
@@ -147,25 +148,34 @@ __device__ __forceinline__ void scaled32(uint32_t at, const float *norms, uint32
     }
 }
 
+// Softmax of half `half` of every tile's keys.  Thread = query.
 template <int D, bool kBF16>
-__device__ void softmax_role(const Params &p, Book &B, uint32_t tmem)
+__device__ void softmax_role(const Params &p, Book &B, int half, uint32_t tmem)
 {
     using C = Cfg<D>;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t o_at = tmem + lanes + C::OCol, q_at = tmem + lanes + C::QCol;
-    const int row = threadIdx.x;                               // query of the run
-    auto fail = [&](unsigned what) {
-        if (lane == 0) atomicOr(&g_status, what);
+    const uint32_t o_at = tmem + lanes + C::OCol + half * (D / 2);     // this half's columns of O
+    const uint32_t q_at = tmem + lanes + C::QCol + half * (D / 2);     // and of Q: the high or the low parts
+    const int row = warp * 32 + lane;                          // query of the run
+    const int meet_id = 1 + warp;
+    // a wait that runs out records a bit; the role then goes on without waiting, to
+    // keep meeting its partner
+    bool ok = true;
+    auto wait = [&](uint64_t &bar, uint32_t parity, unsigned what) {
+        if (ok && !mbar_wait_warp_fast(smem_u32(&bar), parity)) {
+            ok = false;
+            if (lane == 0) atomicOr(&g_status, what);
+        }
     };
     // the run's rotated queries (d high parts, d low parts, fp16) into tensor memory
     auto load_q = [&](const Run &r) {
         const bool live = row < r.rows;
         const int64_t q = live ? shared::query_row(p.w, r, row) : 0;
-        const uint4 *src = static_cast<const uint4 *>(p.w.rot) + q * (D / 4);
+        const uint4 *src = static_cast<const uint4 *>(p.w.rot) + q * (D / 4) + half * (D / 8);
         if (warp * 32 < r.rows) {
-#pragma unroll
-            for (int c = 0; c < D; c += 32) {
+#pragma unroll 1
+            for (int c = 0; c < D / 2; c += 32) {
                 uint32_t v[32];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -189,41 +199,46 @@ __device__ void softmax_role(const Params &p, Book &B, uint32_t tmem)
     uint32_t i = 0;                                            // tiles of the CTA so far
     while (c.more) {
         const Run r = c.r;
-        const bool idle = warp * 32 >= r.rows;                 // no query of this warp
+        const bool idle = warp * 32 >= r.rows;                 // no query of these warps
         float m = -INFINITY, l = 0.0f;
         for (int k = 0; k < r.tiles; ++k, ++i) {
             const int buf = i & 1;
-            if (!mbar_wait_warp(smem_u32(&B.s_full[buf]), (i >> 1) & 1)) return fail(kErrTimeoutMma);
+            wait(B.s_full[buf], (i >> 1) & 1, kErrTimeoutMma);
             tc_fence_after_sync();
             if (k + 1 == r.tiles) {                            // all products with this run's Q are done
                 c.next_run();
                 if (c.more) rs_next = load_q(c.r);
             }
-            if (!mbar_wait_warp(smem_u32(&B.n_full[i & 3]), (i >> 2) & 1)) return fail(kErrTimeoutDrain);
+            wait(B.n_full[i & 3], (i >> 2) & 1, kErrTimeoutDrain);
             if (!idle) {
                 const uint32_t s_at = tmem + lanes + buf * kTile;
-                const float *norms = B.norms[i & 3];
+                const float *norms = B.norms[i & 3] + 64 * half;
                 const int lim = r.keys - (r.tile + k) * kTile; // keys of the tile
+                const uint32_t s_half = s_at + 64 * half;      // this half's scores
                 float mx = -INFINITY;
-#pragma unroll 1
-                for (int e = 0; e < kTile; e += 32) {
+#pragma unroll
+                for (int e = 0; e < 64; e += 32) {
                     uint32_t s[32];
-                    scaled32(s_at + e, norms + e, s);
-                    if (lim < kTile) mask32(s, lim - e);
+                    scaled32(s_half + e, norms + e, s);
+                    if (lim < kTile) mask32(s, lim - 64 * half - e);
                     mx = max32(s, mx);
                 }
+                float(*word)[kQueries] = B.word[i & 1];
+                word[half][row] = mx;
+                meet_partner(meet_id);
+                mx = fmaxf(mx, word[half ^ 1][row]);
                 if (k == 0) {
                     m = mx;
                 } else if (__any_sync(0xffffffffu, (mx - m) * rs > kLazy)) {
-                    // the last P V must be complete before O is rescaled
-                    if (!mbar_wait_warp(smem_u32(&B.o_done), (i - 1) & 1)) return fail(kErrTimeoutMma);
+                    // both warps see the same maxima; the last P V must be complete before O is rescaled
+                    wait(B.o_done, (i - 1) & 1, kErrTimeoutMma);
                     tc_fence_after_sync();
                     const float up = fmaxf(m, mx);
                     const float f = m == -INFINITY ? 0.0f : ex2((m - up) * rs);
                     m = up;
                     l *= f;
 #pragma unroll 1
-                    for (int e = 0; e < D; e += 32) {
+                    for (int e = 0; e < D / 2; e += 32) {
                         uint32_t o[32];
                         tmem_ld32(o_at + e, o);
 #pragma unroll
@@ -234,13 +249,13 @@ __device__ void softmax_role(const Params &p, Book &B, uint32_t tmem)
                 const float c0 = m == -INFINITY ? 0.0f : kBias<kBF16> - m * rs;
                 const uint64_t scale2 = pair(rs, rs), c2 = pair(c0, c0);
                 uint64_t sum0 = pair(l, 0.0f), sum1 = pair(0.0f, 0.0f);
-#pragma unroll 1
-                for (int e = 0; e < kTile; e += 32) {
+#pragma unroll
+                for (int e = 0; e < 64; e += 32) {
                     uint32_t s[32], w[16];
-                    scaled32(s_at + e, norms + e, s);
-                    if (lim < kTile) mask32(s, lim - e);
-                    weights32<kBF16>(s, scale2, c2, sum0, sum1, w);
-                    tmem_st16(s_at + e / 2, w);                // over scores that are read already
+                    scaled32(s_half + e, norms + e, s);
+                    if (lim < kTile) mask32(s, lim - 64 * half - e);
+                    weights32<kBF16, kPolyShare>(s, scale2, c2, sum0, sum1, w);
+                    tmem_st16(s_half + e / 2, w);              // over scores that are read already
                 }
                 float s0, s1, s2, s3;
                 unpair(sum0, s0, s1);
@@ -248,29 +263,37 @@ __device__ void softmax_role(const Params &p, Book &B, uint32_t tmem)
                 l = (s0 + s1) + (s2 + s3);
                 tmem_wait_st();
                 tc_fence_before_sync();
+                // A wait tells a phase only from its neighbours, and the last two P V could
+                // both be running, or both be complete, at the wait below: see the last but
+                // one complete before the last can start.
+                if (i > 0 && k + 1 == r.tiles) wait(B.o_done, (i - 1) & 1, kErrTimeoutMma);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&B.p_full[buf]));
         }
-        // the last two P V in turn: both may still be running, and a wait tells a phase
-        // only from its neighbours
-        if (i > 1 && !mbar_wait_warp(smem_u32(&B.o_done), (i - 2) & 1)) return fail(kErrTimeoutMma);
-        if (!mbar_wait_warp(smem_u32(&B.o_done), (i - 1) & 1)) return fail(kErrTimeoutMma);
         if (!idle) {
+            wait(B.o_done, (i - 1) & 1, kErrTimeoutMma);
             tc_fence_after_sync();
+            float(*word)[kQueries] = B.word[i & 1];            // the other half's sum
+            word[half][row] = l;
+            meet_partner(meet_id);
+            l += word[half ^ 1][row];
+            // nobody writes the words again before both have read them
+            meet_partner(meet_id);
             float *dst = shared::slot(p.w, r, blockIdx.x, row);
             const bool live = row < r.rows && AXR_IN((r.seq >= 0 ? p.w.sp_own_part : p.w.sp_prefix_part), dst, (D + 2) * 4);
-#pragma unroll
-            for (int e = 0; e < D; e += 32) {
+#pragma unroll 1
+            for (int e = 0; e < D / 2; e += 32) {
                 uint32_t o[32];
                 tmem_ld32(o_at + e, o);
                 if (live) {
 #pragma unroll
                     for (int y = 0; y < 32; y += 2)
-                        *reinterpret_cast<uint2 *>(dst + e + y) = make_uint2(o[y], o[y + 1]);
+                        *reinterpret_cast<uint2 *>(dst + half * (D / 2) + e + y) = make_uint2(o[y], o[y + 1]);
                 }
             }
-            if (live) *reinterpret_cast<float2 *>(dst + D) = make_float2(m == -INFINITY ? m : m * rs - kBias<kBF16>, l);
+            if (live && half == 0)
+                *reinterpret_cast<float2 *>(dst + D) = make_float2(m == -INFINITY ? m : m * rs - kBias<kBF16>, l);
             tc_fence_before_sync();
         }
         rs = rs_next;
@@ -334,17 +357,18 @@ __device__ __forceinline__ uint4 centroids(uint32_t nib, const uint32_t (&lo)[2]
     return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-// Thread = key of the tile.
+// Thread = key of the tile; `half` of its coordinates.
 template <int D, int B>
-__device__ void code_role(const Params &p, Book &S, uint8_t *k_smem)
+__device__ void code_role(const Params &p, Book &S, int half, uint8_t *k_smem)
 {
     using C = Cfg<D>;
-    constexpr int P = D * B / 8, W = (P + 3) / 4;              // a packed row in bytes and words
-    const int key = threadIdx.x - 128, lane = threadIdx.x & 31;
+    constexpr int P = D * B / 8, H = P / 2, W = (H + 3) / 4;   // a packed row, half of it, in words
+    constexpr int U = P % 32 == 0 ? 16 : P % 16 == 0 ? 8 : 4;  // bytes of a load: rows and halves are so aligned
+    const int key = threadIdx.x & 127, lane = threadIdx.x & 31;
     Cursor c(p.w, S);
     uint32_t row[W + 1], ahead[W];
     float norm_ahead = 0.0f;
-    // the packed row and norm of the cursor's tile, zeros past its keys
+    // the packed half row and the norm of the cursor's tile, zeros past its keys
     auto fetch = [&](uint32_t (&to)[W], float &norm) {
 #pragma unroll
         for (int i = 0; i < W; ++i) to[i] = 0u;
@@ -352,24 +376,23 @@ __device__ void code_role(const Params &p, Book &S, uint8_t *k_smem)
         if (!c.more || key >= c.keys()) return;
         const bool own = c.r.seq >= 0;
         const int64_t at = c.r.base + static_cast<int64_t>(c.tile()) * kTile + key;
-        const uint8_t *src = (own ? p.idx : p.prefix_idx) + at * P;
+        const uint8_t *src = (own ? p.idx : p.prefix_idx) + at * P + half * H;
         const float *ns = (own ? p.norms : p.prefix_norms) + at;
-        if (AXR_IN((own ? p.sp_idx : p.sp_prefix_idx), src, P)) {
-            if constexpr (P % 16 == 0) {
+        if (AXR_IN((own ? p.sp_idx : p.sp_prefix_idx), src, H)) {
 #pragma unroll
-                for (int i = 0; i < P / 16; ++i) {
+            for (int i = 0; i < H / U; ++i) {
+                if constexpr (U == 16) {
                     const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(src) + i);
                     to[4 * i] = v.x; to[4 * i + 1] = v.y; to[4 * i + 2] = v.z; to[4 * i + 3] = v.w;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < P / 8; ++i) {
+                } else if constexpr (U == 8) {
                     const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(src) + i);
                     to[2 * i] = v.x; to[2 * i + 1] = v.y;
+                } else {
+                    to[i] = __ldcs(reinterpret_cast<const uint32_t *>(src) + i);
                 }
             }
         }
-        if (AXR_IN((own ? p.sp_norms : p.sp_prefix_norms), ns, 4)) norm = __ldcs(ns);
+        if (half == 0 && AXR_IN((own ? p.sp_norms : p.sp_prefix_norms), ns, 4)) norm = __ldcs(ns);
     };
     const uint32_t lo[2] = {p.lo[0], p.lo[1]}, hi[2] = {p.hi[0], p.hi[1]};
     fetch(ahead, norm_ahead);
@@ -381,26 +404,28 @@ __device__ void code_role(const Params &p, Book &S, uint8_t *k_smem)
         c.next();
         fetch(ahead, norm_ahead);                              // lands while this tile is looked up
         const int buf = i & 1;
-        if (!mbar_wait_warp(smem_u32(&S.k_empty[buf]), ((i >> 1) & 1) ^ 1)) {
+        if (!mbar_wait_warp_fast(smem_u32(&S.k_empty[buf]), ((i >> 1) & 1) ^ 1)) {
             if (lane == 0) atomicOr(&g_status, kErrTimeoutMma);
             return;
         }
-        // written before S of tile i - 2, whose norms this slot's neighbours hold
-        S.norms[i & 3][key] = norm;
+        // S of tile i - 2 is complete, so the softmax is done with the norms of tile
+        // i - 4 that this slot held
+        if (half == 0) S.norms[i & 3][key] = norm;
         uint8_t *dst = k_smem + buf * C::TileBytes + key * 128;
 #pragma unroll
-        for (int e = 0; e < D / 8; ++e) {
+        for (int e = 0; e < D / 16; ++e) {
             constexpr uint32_t kMask = B == 4 ? 0xffffffffu : (1u << (8 * B)) - 1u;
             const int bit = e * 8 * B, at = bit >> 5, sh = bit & 31;
             const uint32_t w = (sh == 0 ? row[at] : __funnelshift_r(row[at], row[at + 1], sh)) & kMask;
-            *reinterpret_cast<uint4 *>(dst + (e >> 3) * kTile * 128 + (((e & 7) ^ (key & 7)) << 4)) =
+            const int chunk = half * (D / 16) + e;             // of 16 bytes in the key's row of fp16
+            *reinterpret_cast<uint4 *>(dst + (chunk >> 3) * kTile * 128 + (((chunk & 7) ^ (key & 7)) << 4)) =
                 centroids<B>(nibbles<B>(w), lo, hi);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
             mbar_arrive(smem_u32(&S.k_full[buf]));
-            mbar_arrive(smem_u32(&S.n_full[i & 3]));
+            if (half == 0) mbar_arrive(smem_u32(&S.n_full[i & 3]));
         }
     }
 }
@@ -416,7 +441,7 @@ __device__ void mma_role(const Params &p, Book &B, uint8_t *v_ptr, uint32_t k_sm
     Cursor sc(p.w, B), pv(p.w, B);
     uint32_t i = 0, runs = 0;                                  // tiles and runs scored
     auto wait = [&](uint64_t &bar, uint32_t parity, unsigned what) {
-        if (mbar_wait_warp(smem_u32(&bar), parity)) return true;
+        if (mbar_wait_warp_fast(smem_u32(&bar), parity)) return true;
         if (lane == 0) atomicOr(&g_status, what);
         return false;
     };
@@ -459,7 +484,8 @@ __device__ void mma_role(const Params &p, Book &B, uint8_t *v_ptr, uint32_t k_sm
         if (elect_one()) {
 #pragma unroll
             for (int e = 0; e < kTile / 16; ++e)
-                mma_f16_ts(tmem + C::OCol, tmem + buf * kTile + e * 8,
+                mma_f16_ts(tmem + C::OCol, tmem + buf * kTile + (e & 4) * 16 + (e & 3) * 8,   // each half's weights lie where its scores were
+                          
                            desc_mn_sw128(v_smem + s * C::TileBytes + e * 2048, kTile * 128), kIdO, pv.k > 0 || e > 0);
             mma_commit(smem_u32(&B.v_empty[s]));
             mma_commit(smem_u32(&B.o_done));
@@ -511,13 +537,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
             mbar_init(smem_u32(&B.v_empty[s]), 1);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(smem_u32(&B.k_full[s]), 4);
+            mbar_init(smem_u32(&B.k_full[s]), kCodeWarps);
             mbar_init(smem_u32(&B.k_empty[s]), 1);
             mbar_init(smem_u32(&B.s_full[s]), 1);
-            mbar_init(smem_u32(&B.p_full[s]), 4);
+            mbar_init(smem_u32(&B.p_full[s]), 8);
         }
         for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&B.n_full[s]), 4);
-        mbar_init(smem_u32(&B.q_full), 4);
+        mbar_init(smem_u32(&B.q_full), 8);
         mbar_init(smem_u32(&B.o_done), 1);
         mbar_init(smem_u32(&B.drain), 1);
         fence_mbar_init();
@@ -535,13 +561,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = B.tmem_base;
-    if (warp < 4) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        softmax_role<D, kBF16>(p, B, tmem);
-    } else if (warp < 8) {
-        code_role<D, NB>(p, B, smem);
+    if (warp < 8) {
+        softmax_role<D, kBF16>(p, B, warp >> 2, tmem);
+    } else if (warp < kWarpMma) {
+        code_role<D, NB>(p, B, (warp >> 2) & 1, smem);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kWarpMma) mma_role<D, kBF16>(p, B, v_ptr, smem_u32(smem), smem_u32(v_ptr), tmem);
         else if (warp == kWarpTma) tma_role<D>(p, B, smem_u32(v_ptr));
     }

@@ -137,20 +137,21 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity)
 
 // The same wait on the critical path of a pipeline: try_wait as it comes, without
 // the long suspension, whose end costs more time than the wait.
-__device__ __forceinline__ bool mbar_wait_warp_fast(uint32_t bar, uint32_t parity)
+__device__ __forceinline__ bool mbar_wait_fast(uint32_t bar, uint32_t parity)
 {
-    bool ok = true;
     unsigned long long t0 = 0;
     for (uint32_t i = 0; !mbar_try_wait(bar, parity); ++i) {
         if ((i & 63u) != 63u) continue;
         const unsigned long long t = globaltimer();
         if (t0 == 0) t0 = t;
-        else if (t - t0 > kWaitNs) {
-            ok = false;
-            break;
-        }
+        else if (t - t0 > kWaitNs) return false;
     }
-    return __all_sync(0xffffffffu, ok) != 0;
+    return true;
+}
+
+__device__ __forceinline__ bool mbar_wait_warp_fast(uint32_t bar, uint32_t parity)
+{
+    return __all_sync(0xffffffffu, mbar_wait_fast(bar, parity)) != 0;
 }
 
 // 2-D tiled TMA load of one box into shared memory, completing on `bar`.

@@ -1,9 +1,17 @@
 // Softmax arithmetic of the tensor-core attention kernels: one thread holds a
-// query's scores of a tile in registers and turns them into 16-bit weights.
+// query's scores of a quarter tile of keys in registers and turns them into 16-bit
+// weights.  Two threads share a query, each with half of a tile's keys: that halves
+// the time from scores to weights, which the products of the same tile wait for,
+// and leaves enough warps on an SM to hide each other's latencies.  The scores are
+// read from tensor memory twice, for the maximum and for the weights: held in
+// registers in between they spilled, and with shared memory full the spills went
+// to L2.
 #pragma once
 
 #include <cstdint>
 #include <cuda_runtime.h>
+
+#include "sm100.cuh"
 
 namespace axr {
 namespace softmax {
@@ -71,21 +79,20 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return r;
 }
 
-// The tile loops below are rolled into chunks of 32 columns on purpose: unrolled
-// over a tile their code is streamed through the instruction caches once a tile,
-// and every other role of the SM waits for instructions.
-
 // largest of 32 scores and `m`
 __device__ __forceinline__ float max32(const uint32_t (&s)[32], float m)
 {
-    float top[2] = {m, __uint_as_float(s[0])};
+    float top[4];
 #pragma unroll
-    for (int i = 1; i < 29; i += 4) {
-        top[0] = max3(top[0], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-        top[1] = max3(top[1], __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
-    }
-    top[0] = max3(top[0], __uint_as_float(s[29]), __uint_as_float(s[30]));
-    return max3(top[0], top[1], __uint_as_float(s[31]));
+    for (int e = 0; e < 4; ++e)
+        top[e] = max3(__uint_as_float(s[3 * e]), __uint_as_float(s[3 * e + 1]), __uint_as_float(s[3 * e + 2]));
+#pragma unroll
+    for (int i = 12; i < 28; i += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top[e] = max3(top[e], __uint_as_float(s[i + 2 * e]), __uint_as_float(s[i + 2 * e + 1]));
+    top[0] = max3(top[0], __uint_as_float(s[28]), __uint_as_float(s[29]));
+    top[1] = max3(top[1], __uint_as_float(s[30]), __uint_as_float(s[31]));
+    return max3(max3(top[0], top[1], top[2]), top[3], m);
 }
 
 // scores from column `lim` on to -inf
@@ -96,8 +103,33 @@ __device__ __forceinline__ void mask32(uint32_t (&s)[32], int lim)
         if (c >= lim) s[c] = 0xff800000u;
 }
 
-// Softmax of 32 scores: p = 2^(s * scale + c), their sum into (sum0, sum1), packed into w
-template <bool kBF16>
+// 2^x of a pair on the FMA pipes, for x <= 127: x = n + f with n whole and
+// |f| <= 1/2 (the sum with 1.5 * 2^23 rounds x to n, and its low bits are n), a
+// polynomial for 2^f, and n added to the exponent.  The coefficients minimise the
+// largest relative error of degree 4 over [-1/2, 1/2], 2.6e-6 (mean 1.4e-8).
+// Below 2^-126, at -inf too, the result is 2^-126.
+__device__ __forceinline__ void exp2_poly(float &x, float &y)
+{
+    constexpr float kRound = 12582912.0f;
+    const uint64_t v = pair(fmaxf(x, -126.0f), fmaxf(y, -126.0f));
+    const uint64_t t = add2(v, pair(kRound, kRound));
+    const uint64_t f = fma2(add2(t, pair(-kRound, -kRound)), pair(-1.0f, -1.0f), v);
+    uint64_t r = fma2(f, pair(0.009570086374878883f, 0.009570086374878883f), pair(0.055917851626873016f, 0.055917851626873016f));
+    r = fma2(f, r, pair(0.240247443318367f, 0.240247443318367f));
+    r = fma2(f, r, pair(0.6931217908859253f, 0.6931217908859253f));
+    r = fma2(f, r, pair(0.9999992847442627f, 0.9999992847442627f));
+    float tx, ty, rx, ry;
+    unpair(t, tx, ty);
+    unpair(r, rx, ry);
+    x = __uint_as_float((__float_as_uint(tx) << 23) + __float_as_uint(rx));
+    y = __uint_as_float((__float_as_uint(ty) << 23) + __float_as_uint(ry));
+}
+
+// Softmax of 32 scores: p = 2^(s * scale + c), their sum into (sum0, sum1),
+// packed into w.  kPoly of every 8 pairs take the polynomial: the special function
+// unit gives 16 results a cycle and SM, 1024 cycles for a tile, as long as the
+// tile's products take.
+template <bool kBF16, int kPoly>
 __device__ __forceinline__ void weights32(const uint32_t (&s)[32], uint64_t scale2, uint64_t c2, uint64_t &sum0,
                                           uint64_t &sum1, uint32_t (&w)[16])
 {
@@ -105,12 +137,25 @@ __device__ __forceinline__ void weights32(const uint32_t (&s)[32], uint64_t scal
     for (int i = 0; i < 32; i += 2) {
         float a, b;
         unpair(fma2(pair(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), scale2, c2), a, b);
-        a = ex2(a);
-        b = ex2(b);
+        if (kPoly > 0 && (i / 2) * kPoly % 8 + kPoly > 7) {
+            exp2_poly(a, b);
+        } else {
+            a = ex2(a);
+            b = ex2(b);
+        }
         if (i & 2) sum1 = add2(sum1, pair(a, b));
         else sum0 = add2(sum0, pair(a, b));
         w[i / 2] = pack16<kBF16>(a, b);
     }
+}
+
+// A barrier of the two warps that share the 32 queries of a lane quadrant, each
+// with one half of a tile's keys: they agree on a maximum (every tile) and add
+// their sums (at the end).  It has no time limit, so a role whose other waits ran
+// out keeps coming here.
+__device__ __forceinline__ void meet_partner(int id)
+{
+    asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
 }
 
 }  // namespace softmax
