@@ -328,7 +328,8 @@ int axr_prompt_attention(const void *q, const void *K, const void *V, int dtype,
  * lse           device float[batch*heads*group], or NULL.
  * Codes and V 16-byte aligned, norms 4-byte (either set may be NULL when its n or
  * capacity is 0).  d a power of two in [32, 512]; b in [1, 4]; group in [1, 8];
- * n and capacity at most 2^31 - 129; at most 2^31 - 1 query rows.  Sums and softmax are
+ * n and capacity at most 2^31 - 129; at most 2^31 - 1 query rows; at most 2^31 - 1
+ * tiles of 128 keys (plus a few a run) over all KV heads and sequences.  Sums and softmax are
  * fp32; out is rounded to vdtype once.  Three kernels on `stream`.
  */
 int axr_attention_shared_workspace_bytes(int batch, int heads, int group, int d, int64_t *bytes);

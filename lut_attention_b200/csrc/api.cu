@@ -582,6 +582,7 @@ extern "C" int axr_attention_shared(const void *q, int qdtype, const uint8_t *pr
     SharedArgs a{q, qdtype, prefix_idx, prefix_norms, prefix_V, n, idx, norms, V, capacity, lengths, vdtype, batch,
                  heads, group, d, b, signs, workspace, out, lse, Codebook{}};
     if (!get_codebook(d, b, &a.cb)) return fail(AXR_EUNSUPPORTED, "no codebook for d=%d b=%d", d, b);
+    if (!shared_fits(a)) return fail(AXR_EUNSUPPORTED, "more than 2^31-1 tiles of 128 keys over all heads and sequences");
     const cudaError_t e = launch_shared_attention(a, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(AXR_ECUDA, "shared-prefix attention launch: %s", cudaGetErrorString(e));
     return ok();

@@ -42,7 +42,7 @@ using namespace softmax;
 
 constexpr int kTile = 128;                     // queries of a tile, keys of a tile
 constexpr int kMaxStages = 12;
-constexpr int kPolyShare = 3;                  // of 8 pairs of exponentials on the FMA pipes
+constexpr int kPolyShare = 2;                  // of 8 pairs of exponentials on the FMA pipes
 
 __device__ unsigned int g_status;
 
@@ -156,15 +156,21 @@ __device__ void softmax_role(const Params &p, Book &B, int t, int half, uint32_t
                 const uint32_t s_at = tmem + lanes + buf * kTile;
                 const uint32_t s_half = s_at + 64 * half;      // this half's scores
                 const int seen = first + past + 1 - j * kTile; // keys of the tile that the warps' first query sees
-                const int lim = seen + lane - 64 * half;       // of this half that this query sees
-                float mx = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < 64; c += 32) {
-                    uint32_t s[32];
-                    tmem_ld32(s_half + c, s);
-                    if (seen < kTile) mask32(s, lim - c);
-                    mx = max32(s, mx);
+                if (seen < kTile) {                            // a tile on the diagonal, or the last: rare
+#pragma unroll 1
+                    for (int c = 0; c < 64; c += 32) {
+                        uint32_t x[32];
+                        tmem_ld32(s_half + c, x);
+                        mask32(x, seen + lane - 64 * half - c);
+                        tmem_st32(s_half + c, x);
+                    }
+                    tmem_wait_st();
                 }
+                uint32_t s[32];
+                tmem_ld32(s_half + 32, s);
+                float mx = max32(s, -INFINITY);
+                tmem_ld32(s_half, s);                          // kept for the weights
+                mx = max32(s, mx);
                 float(*word)[kTile] = B.word[C::NQ == 2 ? t : count & 1];
                 word[half][r] = mx;
                 meet_partner(meet_id);
@@ -192,14 +198,12 @@ __device__ void softmax_role(const Params &p, Book &B, int t, int half, uint32_t
                 const float c0 = m == -INFINITY ? 0.0f : kBias<kBF16> - m * p.scale;
                 const uint64_t scale2 = pair(p.scale, p.scale), c2 = pair(c0, c0);
                 uint64_t sum0 = pair(l, 0.0f), sum1 = pair(0.0f, 0.0f);
-#pragma unroll
-                for (int c = 0; c < 64; c += 32) {
-                    uint32_t s[32], w[16];
-                    tmem_ld32(s_half + c, s);
-                    if (seen < kTile) mask32(s, lim - c);
-                    weights32<kBF16, kPolyShare>(s, scale2, c2, sum0, sum1, w);
-                    tmem_st16(s_half + c / 2, w);              // over scores that are read already
-                }
+                uint32_t w[16];
+                weights32<kBF16, kPolyShare>(s, scale2, c2, sum0, sum1, w);
+                tmem_ld32(s_half + 32, s);
+                tmem_st16(s_half, w);                          // over scores that are read already
+                weights32<kBF16, kPolyShare>(s, scale2, c2, sum0, sum1, w);
+                tmem_st16(s_half + 16, w);
                 float s0, s1, s2, s3;
                 unpair(sum0, s0, s1);
                 unpair(sum1, s2, s3);

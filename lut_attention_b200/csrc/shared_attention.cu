@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kBeforeWarps * 32) before_kernel(const BeforeP
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
     const int64_t rows = static_cast<int64_t>(p.w.batch) * p.w.heads * p.w.group;
-    if (blockIdx.x == 0) {                                    // tile counts of the own keys, summed over the batch
+    if (blockIdx.x == 0) {                                    // places of the own keys, summed over the batch
         if (threadIdx.x >= 32) return;
         int before = 0;
         for (int b0 = 0; b0 < p.w.batch; b0 += 32) {
@@ -90,15 +90,15 @@ __global__ void __launch_bounds__(kBeforeWarps * 32) before_kernel(const BeforeP
             int len = 0;
             if (b < p.w.batch && AXR_IN(p.w.sp_lengths, p.w.lengths + b, 4)) len = p.w.lengths[b];
             len = min(max(len, 0), p.w.capacity);
-            const int tiles = (len + shared::kTileKeys - 1) / shared::kTileKeys;
-            int upto = tiles;
+            const int mine = shared::places(p.w, len);
+            int upto = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int x = __shfl_up_sync(0xffffffffu, upto, o);
                 if (lane >= o) upto += x;
             }
             int *dst = p.w.own_start + b;
-            if (b < p.w.batch && AXR_IN(p.w.sp_own_start, dst, 4)) *dst = before + upto - tiles;
+            if (b < p.w.batch && AXR_IN(p.w.sp_own_start, dst, 4)) *dst = before + upto - mine;
             before += __shfl_sync(0xffffffffu, upto, 31);
         }
         int *dst = p.w.own_start + p.w.batch;
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kAfterWarps * 32) after_kernel(const AfterPara
     const int g = static_cast<int>(row % w.group);
     const int64_t sh = row / w.group;                         // sequence * heads + head
     const int h = static_cast<int>(sh % w.heads), b = static_cast<int>(sh / w.heads);
-    const Line x = shared::line_of(w);
+    const Line x = shared::line_of(w, shared::own_start(w, w.batch));
 
     float m = -INFINITY, l = 0.0f, o[E];
 #pragma unroll
@@ -204,17 +204,17 @@ __global__ void __launch_bounds__(kAfterWarps * 32) after_kernel(const AfterPara
         for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], a, v[e] * c);
         m = top;
     };
-    if (x.prefix_tiles > 0) {
+    if (x.prefix_places > 0) {
         const int at = b * w.group + g;
-        const int64_t seg = static_cast<int64_t>(h) * w.row_tiles + at / w.bm;
-        const int c0 = x.owner(seg * x.prefix_tiles), c1 = x.owner((seg + 1) * x.prefix_tiles - 1);
+        const int seg = h * w.row_tiles + at / w.bm;
+        const int c0 = x.owner(seg * x.prefix_places + w.run_cost), c1 = x.owner((seg + 1) * x.prefix_places - 1);
         for (int c = c0 + warp; c <= c1; c += kAfterWarps)
-            add(w.prefix_part + ((seg + c) * w.slot_rows + at % w.bm) * (D + 2) AXR_DEBUG_ONLY(, w.sp_prefix_part));
+            add(w.prefix_part + (static_cast<int64_t>(seg + c) * w.slot_rows + at % w.bm) * (D + 2) AXR_DEBUG_ONLY(, w.sp_prefix_part));
     }
     const int s0 = shared::own_start(w, b), per = shared::own_start(w, b + 1) - s0;
     if (per > 0) {
-        const int64_t t0 = x.own_first + static_cast<int64_t>(w.heads) * s0 + static_cast<int64_t>(h) * per;
-        const int c0 = x.owner(t0), c1 = x.owner(t0 + per - 1);
+        const int t0 = x.own_first + w.heads * s0 + h * per;
+        const int c0 = x.owner(t0 + w.run_cost), c1 = x.owner(t0 + per - 1);
         for (int c = c0 + warp; c <= c1; c += kAfterWarps)
             add(w.own_part + ((sh + c) * w.group + g) * (D + 2) AXR_DEBUG_ONLY(, w.sp_own_part));
     }
@@ -263,9 +263,10 @@ __device__ void take_run(const MainParams &p, const Run &r, float *smem, const f
     core::Tile<D, BM> t(smem);
     const Work &w = p.w;
     const bool own = r.seq >= 0;
-    const uint8_t *idx = (own ? p.idx : p.prefix_idx) + r.base * P;
-    const float *norms = (own ? p.norms : p.prefix_norms) + r.base;
-    const T *V = static_cast<const T *>(own ? p.V : p.prefix_V) + r.base * D;
+    const int64_t base = r.base(w);
+    const uint8_t *idx = (own ? p.idx : p.prefix_idx) + base * P;
+    const float *norms = (own ? p.norms : p.prefix_norms) + base;
+    const T *V = static_cast<const T *>(own ? p.V : p.prefix_V) + base * D;
     AXR_DEBUG_ONLY(const dbg::Span sp_i = own ? p.sp_idx : p.sp_prefix_idx;
                    const dbg::Span sp_n = own ? p.sp_norms : p.sp_prefix_norms;
                    const dbg::Span sp_v = own ? p.sp_V : p.sp_prefix_V;)
@@ -337,15 +338,17 @@ __global__ void __launch_bounds__(core::kThreads) main_kernel(const MainParams p
     extern __shared__ float4 smem4[];
     __shared__ float cent[kMaxLevels];
     if (threadIdx.x < (1 << B)) cent[threadIdx.x] = p.cent[threadIdx.x];
-    const Line x = shared::line_of(p.w);
+    const Line x = shared::line_of(p.w, shared::own_start(p.w, p.w.batch));
     if (blockIdx.x >= x.ctas) return;
     float *smem = reinterpret_cast<float *>(smem4);
-    const int64_t end = x.begin(blockIdx.x + 1);
-    for (int64_t t = x.begin(blockIdx.x); t < end;) {
+    const int end = x.begin(blockIdx.x + 1);
+    for (int t = x.begin(blockIdx.x); t < end;) {
         const Run r = shared::run_at(p.w, x, t, end);
-        if (r.seq >= 0) take_run<D, B, kOwnRows, T>(p, r, smem, cent);
-        else take_run<D, B, D <= 128 ? kPrefixRows : 32, T>(p, r, smem, cent);
-        t += r.tiles;
+        if (r.tiles > 0) {
+            if (r.seq >= 0) take_run<D, B, kOwnRows, T>(p, r, smem, cent);
+            else take_run<D, B, D <= 128 ? kPrefixRows : 32, T>(p, r, smem, cent);
+        }
+        t = r.next;
     }
 }
 
@@ -414,7 +417,7 @@ Work work_of(int batch, int heads, int group, int d)
     w.row_tiles = (rows + w.bm - 1) / w.bm;
     w.slot_rows = rows < w.bm ? rows : w.bm;
     w.ctas = device_sm_count() * (d <= 128 ? 2 : 1);          // as many as are resident
-    w.min_tiles = 1;
+    w.run_cost = 1;
     return w;
 }
 
@@ -487,13 +490,24 @@ int64_t shared_workspace_bytes(int batch, int heads, int group, int d)
     return core > tc ? core : tc;
 }
 
-cudaError_t launch_shared_attention(const SharedArgs &a, cudaStream_t stream)
+namespace {
+Work work_for(const SharedArgs &a)
 {
-    const bool tc = shared_tc_supported(a);
-    Work w = tc ? shared_tc_work(a.batch, a.heads, a.group, a.d) : work_of(a.batch, a.heads, a.group, a.d);
+    Work w = shared_tc_supported(a) ? shared_tc_work(a.batch, a.heads, a.group, a.d)
+                                    : work_of(a.batch, a.heads, a.group, a.d);
     w.n = static_cast<int>(a.n);
     w.capacity = static_cast<int>(a.capacity);
     w.lengths = a.lengths;
+    return w;
+}
+}  // namespace
+
+bool shared_fits(const SharedArgs &a) { return shared::most_places(work_for(a)) <= INT32_MAX; }
+
+cudaError_t launch_shared_attention(const SharedArgs &a, cudaStream_t stream)
+{
+    const bool tc = shared_tc_supported(a);
+    Work w = work_for(a);
     shared::lay_out(w, a.workspace);
     cudaError_t e = launch_shared_before(a, w, tc, stream);
     if (e != cudaSuccess) return e;

@@ -2,14 +2,15 @@
 // cores (axr_attention_shared for 16-bit values, d = 64 and 128).  Per tile of 128
 // keys and up to 128 queries (a block of the batch * group queries of a KV head
 // against the prefix, or the group's queries against a sequence's own keys):
-//     S = (Q_hi + Q_lo) C^T              C: the keys' centroids, fp16 in shared memory
-//     x_t = S_t norm_t,  p = 2^(x rs - m)  one thread per query, fp32
+//     S = (Q_hi + Q_lo) C_hi^T + Q_hi C_lo^T   C: the keys' centroids in shared memory
+//     x_t = S_t norm_t,  p = 2^(x rs - m)  two threads per query, fp32
 //     O += P V,  l += sum p                O in tensor memory, P of V's type
-// rs holds the query's own factor and the codebook's (half_codebook.h).  The keys
-// are looked up once for all 128 queries and never multiplied out: a code becomes
-// its centroid, 16 bits picked out of at most 8 by byte permutes, and the norm
-// joins after the product.  The query is split into two fp16 parts (22 bits), so
-// that only the centroids' rounding (at most 2^-13 relatively) is left in S.
+// The keys are looked up once for all 128 queries and never multiplied out: a code
+// becomes its centroid, 16 bits picked out of at most 8 by byte permutes, and the
+// norm joins after the product.  Queries and centroids are pairs of fp16 parts, 22
+// bits: with the centroids' high parts alone (2^-11) their rounding, the same for
+// every key with a code, does not average out, and moved lse by 2e-5 relatively.
+// rs holds the query's factor and the centroids', powers of two.
 //
 // A persistent CTA per SM walks its stretch of tiles (shared.cuh) with
 //   warps 0-7   softmax: Q into tensor memory (an operand from there, which spares
@@ -25,14 +26,12 @@
 //
 // Bound: the codes, norms and values of a tile are 128 (P + 4 + 2d) bytes, 41 KB at
 // d = 128 and b = 4, about 1800 cycles of one SM's share of the memory bandwidth;
-// its products take 3 * 512.
+// its products take 4 * 512.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <mutex>
 
 #include "axr_internal.cuh"
-#include "half_codebook.h"
 #include "shared.cuh"
 #include "sm100.cuh"
 #include "softmax_tc.cuh"
@@ -48,11 +47,13 @@ using shared::Work;
 
 constexpr int kTile = shared::kTileKeys;
 constexpr int kQueries = 128;
+constexpr int kPieceKeys = 64;                 // values come in pieces of half a tile
 constexpr int kCodeWarps = 8;                  // after the eight of the softmax
 constexpr int kWarpMma = 8 + kCodeWarps, kWarpTma = kWarpMma + 1;
 constexpr int kThreads = (kWarpTma + 1) * 32;
-constexpr int kPolyShare = 3;                  // of 8 pairs of exponentials on the FMA pipes
-constexpr int kIndexed = 1024;                 // sequences whose starts and lengths fit shared memory
+constexpr int kRunCost = 3;                    // a run's queries and sums, in tiles
+constexpr int kPolyShare = 2;                  // of 8 pairs of exponentials on the FMA pipes
+constexpr int kIndexed = 256;                  // sequences whose starts and lengths fit shared memory
 
 __device__ unsigned int g_status;
 
@@ -60,12 +61,14 @@ template <int D>
 struct Cfg {
     static constexpr int Blocks = D / 64;                      // 64-element blocks of a row
     static constexpr int TileBytes = kTile * D * 2;            // centroids or values of a tile
+    static constexpr int KBytes = 2 * TileBytes;               // high parts, then low parts
     static constexpr int KStages = 2;
-    static constexpr int VStages = D == 64 ? 8 : 4;
+    static constexpr int PieceBytes = kPieceKeys * D * 2;      // values of half a tile
+    static constexpr int VStages = D == 64 ? 10 : 5;
     static constexpr int OCol = 2 * kTile, QCol = OCol + D;    // tensor memory: two S, O, Q
     static_assert(QCol + D <= 512, "tensor memory");
 };
-constexpr int kMaxV = 8;
+constexpr int kMaxV = 10;
 
 struct Book {
     uint64_t v_full[kMaxV], v_empty[kMaxV];
@@ -73,6 +76,7 @@ struct Book {
     uint64_t s_full[2], p_full[2];
     uint64_t n_full[4];        // norms of a tile are written
     uint64_t q_full, o_done, drain;
+    uint64_t tail;             // a V tile that reaches behind its sequence has landed
     uint32_t tmem_base;
     float word[2][2][kQueries];                                // by turn and half: what they exchange
     alignas(16) float norms[4][kTile];                         // read 16 bytes at a time
@@ -80,17 +84,18 @@ struct Book {
 };
 
 template <int D>
-constexpr size_t smem_bytes() { return 1024 + (Cfg<D>::KStages + Cfg<D>::VStages) * Cfg<D>::TileBytes; }
-static_assert(smem_bytes<128>() + sizeof(Book) <= 232448 && smem_bytes<64>() + sizeof(Book) <= 232448, "shared memory");
+constexpr size_t smem_bytes() { return Cfg<D>::KStages * Cfg<D>::KBytes + Cfg<D>::VStages * Cfg<D>::PieceBytes + sizeof(Book); }
+static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory");
 
 struct Params {
-    CUtensorMap prefix_v, own_v;       // (heads, rows, d), box 64 x 128 rows
+    CUtensorMap prefix_v, own_v;       // (heads, rows, d), box 64 x 64 rows
     Work w;
     const uint8_t *prefix_idx, *idx;
     const float *prefix_norms, *norms;
     float inv_scale;                   // 1 / the codebook's scale
-    // centroids by code: low and high bytes (b = 4: magnitudes of codes 8 .. 15)
-    uint32_t lo[2], hi[2];
+    // the centroids' high and low fp16 parts by code, their low and high bytes (b = 4:
+    // of codes 8 .. 15, the positive ones)
+    uint32_t table[2][2][2];
     AXR_DEBUG_ONLY(dbg::Span sp_prefix_idx, sp_idx, sp_prefix_norms, sp_norms;)
 };
 
@@ -99,33 +104,34 @@ struct Cursor {
     const Work &w;
     const Book &B;
     Line x;
-    int64_t t, end;
+    int t = 0, end = 0;
     Run r;
     int k = 0;                         // tiles of the run passed
     bool more;
 
-    __device__ Cursor(const Work &work, const Book &book) : w(work), B(book), x(shared::line_of(work))
+    __device__ Cursor(const Work &work, const Book &book) : w(work), B(book)
     {
-        t = blockIdx.x < x.ctas ? x.begin(blockIdx.x) : 0;
-        end = blockIdx.x < x.ctas ? x.begin(blockIdx.x + 1) : 0;
+        x = shared::line_of(w, w.batch <= kIndexed ? B.start[w.batch] : shared::own_start(w, w.batch));
+        if (blockIdx.x < x.ctas) {
+            t = x.begin(blockIdx.x);
+            end = x.begin(blockIdx.x + 1);
+        }
         find();
     }
     __device__ void find()
     {
-        more = t < end;
         k = 0;
-        if (!more) return;
-        if (w.batch <= kIndexed) r = shared::run_at(w, x, t, end, [&](int b) { return B.start[b]; }, [&](int b) { return B.len[b]; });
-        else r = shared::run_at(w, x, t, end);
-    }
-    __device__ void next_run()
-    {
-        t += r.tiles;
-        find();
+        do {
+            more = t < end;
+            if (!more) return;
+            if (w.batch <= kIndexed) r = shared::run_at(w, x, t, end, [&](int b) { return B.start[b]; }, [&](int b) { return B.len[b]; });
+            else r = shared::run_at(w, x, t, end);
+            t = r.next;
+        } while (r.tiles == 0);
     }
     __device__ void next()
     {
-        if (++k == r.tiles) next_run();
+        if (++k == r.tiles) find();
     }
     __device__ int tile() const { return r.tile + k; }                         // in its segment
     __device__ int keys() const { return min(kTile, r.keys - tile() * kTile); }
@@ -206,7 +212,7 @@ __device__ void softmax_role(const Params &p, Book &B, int half, uint32_t tmem)
             wait(B.s_full[buf], (i >> 1) & 1, kErrTimeoutMma);
             tc_fence_after_sync();
             if (k + 1 == r.tiles) {                            // all products with this run's Q are done
-                c.next_run();
+                c.find();
                 if (c.more) rs_next = load_q(c.r);
             }
             wait(B.n_full[i & 3], (i >> 2) & 1, kErrTimeoutDrain);
@@ -215,14 +221,21 @@ __device__ void softmax_role(const Params &p, Book &B, int half, uint32_t tmem)
                 const float *norms = B.norms[i & 3] + 64 * half;
                 const int lim = r.keys - (r.tile + k) * kTile; // keys of the tile
                 const uint32_t s_half = s_at + 64 * half;      // this half's scores
-                float mx = -INFINITY;
-#pragma unroll
-                for (int e = 0; e < 64; e += 32) {
-                    uint32_t s[32];
-                    scaled32(s_half + e, norms + e, s);
-                    if (lim < kTile) mask32(s, lim - 64 * half - e);
-                    mx = max32(s, mx);
+                if (lim < kTile) {                             // the segment's last tile
+#pragma unroll 1
+                    for (int e = 0; e < 64; e += 32) {
+                        uint32_t y[32];
+                        tmem_ld32(s_half + e, y);
+                        mask32(y, lim - 64 * half - e);
+                        tmem_st32(s_half + e, y);
+                    }
+                    tmem_wait_st();
                 }
+                uint32_t s[32];
+                scaled32(s_half + 32, norms + 32, s);
+                float mx = max32(s, -INFINITY);
+                scaled32(s_half, norms, s);                    // kept for the weights
+                mx = max32(s, mx);
                 float(*word)[kQueries] = B.word[i & 1];
                 word[half][row] = mx;
                 meet_partner(meet_id);
@@ -249,14 +262,12 @@ __device__ void softmax_role(const Params &p, Book &B, int half, uint32_t tmem)
                 const float c0 = m == -INFINITY ? 0.0f : kBias<kBF16> - m * rs;
                 const uint64_t scale2 = pair(rs, rs), c2 = pair(c0, c0);
                 uint64_t sum0 = pair(l, 0.0f), sum1 = pair(0.0f, 0.0f);
-#pragma unroll
-                for (int e = 0; e < 64; e += 32) {
-                    uint32_t s[32], w[16];
-                    scaled32(s_half + e, norms + e, s);
-                    if (lim < kTile) mask32(s, lim - 64 * half - e);
-                    weights32<kBF16, kPolyShare>(s, scale2, c2, sum0, sum1, w);
-                    tmem_st16(s_half + e / 2, w);              // over scores that are read already
-                }
+                uint32_t w[16];
+                weights32<kBF16, kPolyShare>(s, scale2, c2, sum0, sum1, w);
+                scaled32(s_half + 32, norms + 32, s);
+                tmem_st16(s_half, w);                          // over scores that are read already
+                weights32<kBF16, kPolyShare>(s, scale2, c2, sum0, sum1, w);
+                tmem_st16(s_half + 16, w);
                 float s0, s1, s2, s3;
                 unpair(sum0, s0, s1);
                 unpair(sum1, s2, s3);
@@ -327,35 +338,41 @@ __device__ __forceinline__ uint32_t permute(uint32_t a, uint32_t b, uint32_t sel
     return r;
 }
 
-// The fp16 centroids of eight codes given as nibbles.  Bytes are picked by
-// permutes, four codes at a time, from the table's low and high bytes.  At b = 4
-// the table holds the magnitudes of codes 8 .. 15; code c < 8 is minus that of
-// 15 - c: its three low bits are flipped, and its sign comes from a permute whose
-// selector's top bit (set for c >= 8) replicates the picked byte's sign, 0, while
-// a clear one picks 0x7f.
+// Eight codes, given as nibbles, as selectors of byte permutes.  At b = 4 the table
+// holds the parts of codes 8 .. 15; code c < 8 has those of 15 - c, negated: its
+// three low bits are flipped here, and `flip` gets the sign bits of the high bytes
+// (from a permute whose selector's top bit, set for c >= 8, replicates the picked
+// byte's sign, 0, while a clear one picks 0x7f).
 template <int B>
-__device__ __forceinline__ uint4 centroids(uint32_t nib, const uint32_t (&lo)[2], const uint32_t (&hi)[2])
-{
-    uint32_t out[4];
-    uint32_t pick = nib;
-    if constexpr (B == 4) {
-        const uint32_t neg = ~nib & 0x88888888u;
-        pick = (nib ^ (neg - (neg >> 3))) & 0x77777777u;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t sel = h ? pick >> 16 : pick;
-        const uint32_t l = permute(lo[0], lo[1], sel);
-        uint32_t u = permute(hi[0], hi[1], sel);
+struct Picks {
+    uint32_t sel[2], flip[2];
+    __device__ __forceinline__ explicit Picks(uint32_t nib)
+    {
+        uint32_t pick = nib;
         if constexpr (B == 4) {
-            const uint32_t s = permute(0x7f7f7f7fu, 0x7f7f7f7fu, h ? nib >> 16 : nib);
-            u |= (s << 1) & 0x80808080u;
+            const uint32_t neg = ~nib & 0x88888888u;
+            pick = (nib ^ (neg - (neg >> 3))) & 0x77777777u;
         }
-        out[2 * h] = permute(l, u, 0x5140);
-        out[2 * h + 1] = permute(l, u, 0x7362);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            sel[h] = pick >> (16 * h);
+            flip[h] = B == 4 ? (permute(0x7f7f7f7fu, 0x7f7f7f7fu, nib >> (16 * h)) << 1) & 0x80808080u : 0u;
+        }
     }
-    return make_uint4(out[0], out[1], out[2], out[3]);
-}
+    // the fp16 numbers of the eight codes in a table of low and high bytes
+    __device__ __forceinline__ uint4 from(const uint32_t (&table)[2][2]) const
+    {
+        uint32_t out[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t l = permute(table[0][0], table[0][1], sel[h]);
+            const uint32_t u = permute(table[1][0], table[1][1], sel[h]) ^ flip[h];
+            out[2 * h] = permute(l, u, 0x5140);
+            out[2 * h + 1] = permute(l, u, 0x7362);
+        }
+        return make_uint4(out[0], out[1], out[2], out[3]);
+    }
+};
 
 // Thread = key of the tile; `half` of its coordinates.
 template <int D, int B>
@@ -368,14 +385,15 @@ __device__ void code_role(const Params &p, Book &S, int half, uint8_t *k_smem)
     Cursor c(p.w, S);
     uint32_t row[W + 1], ahead[W];
     float norm_ahead = 0.0f;
-    // the packed half row and the norm of the cursor's tile, zeros past its keys
+    // the packed half row and the norm of the cursor's tile; past its keys zeros and a
+    // norm of 1, which a masked score of -inf survives
     auto fetch = [&](uint32_t (&to)[W], float &norm) {
 #pragma unroll
         for (int i = 0; i < W; ++i) to[i] = 0u;
-        norm = 0.0f;
+        norm = 1.0f;
         if (!c.more || key >= c.keys()) return;
         const bool own = c.r.seq >= 0;
-        const int64_t at = c.r.base + static_cast<int64_t>(c.tile()) * kTile + key;
+        const int64_t at = c.r.base(p.w) + static_cast<int64_t>(c.tile()) * kTile + key;
         const uint8_t *src = (own ? p.idx : p.prefix_idx) + at * P + half * H;
         const float *ns = (own ? p.norms : p.prefix_norms) + at;
         if (AXR_IN((own ? p.sp_idx : p.sp_prefix_idx), src, H)) {
@@ -394,7 +412,6 @@ __device__ void code_role(const Params &p, Book &S, int half, uint8_t *k_smem)
         }
         if (half == 0 && AXR_IN((own ? p.sp_norms : p.sp_prefix_norms), ns, 4)) norm = __ldcs(ns);
     };
-    const uint32_t lo[2] = {p.lo[0], p.lo[1]}, hi[2] = {p.hi[0], p.hi[1]};
     fetch(ahead, norm_ahead);
     row[W] = 0u;
     for (uint32_t i = 0; c.more; ++i) {
@@ -411,15 +428,17 @@ __device__ void code_role(const Params &p, Book &S, int half, uint8_t *k_smem)
         // S of tile i - 2 is complete, so the softmax is done with the norms of tile
         // i - 4 that this slot held
         if (half == 0) S.norms[i & 3][key] = norm;
-        uint8_t *dst = k_smem + buf * C::TileBytes + key * 128;
+        uint8_t *dst = k_smem + buf * C::KBytes + key * 128;
 #pragma unroll
         for (int e = 0; e < D / 16; ++e) {
             constexpr uint32_t kMask = B == 4 ? 0xffffffffu : (1u << (8 * B)) - 1u;
             const int bit = e * 8 * B, at = bit >> 5, sh = bit & 31;
             const uint32_t w = (sh == 0 ? row[at] : __funnelshift_r(row[at], row[at + 1], sh)) & kMask;
             const int chunk = half * (D / 16) + e;             // of 16 bytes in the key's row of fp16
-            *reinterpret_cast<uint4 *>(dst + (chunk >> 3) * kTile * 128 + (((chunk & 7) ^ (key & 7)) << 4)) =
-                centroids<B>(nibbles<B>(w), lo, hi);
+            uint4 *to = reinterpret_cast<uint4 *>(dst + (chunk >> 3) * kTile * 128 + (((chunk & 7) ^ (key & 7)) << 4));
+            const Picks<B> picks(nibbles<B>(w));
+            to[0] = picks.from(p.table[0]);
+            to[C::TileBytes / 16] = picks.from(p.table[1]);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -430,106 +449,150 @@ __device__ void code_role(const Params &p, Book &S, int half, uint8_t *k_smem)
     }
 }
 
+// The products, issued by one thread.
 template <int D, bool kBF16>
-__device__ void mma_role(const Params &p, Book &B, uint8_t *v_ptr, uint32_t k_smem, uint32_t v_smem, uint32_t tmem)
+__device__ void issue_products(const Params &p, Book &B, uint32_t k_smem, uint32_t v_smem, uint32_t tmem)
 {
     using C = Cfg<D>;
     constexpr uint32_t kFmt = kBF16 ? kFmtBF16 : kFmtF16;
     constexpr uint32_t kIdS = idesc(kAccF32, kFmtF16, kFmtF16, kQueries, kTile);
     constexpr uint32_t kIdO = idesc(kAccF32, kFmt, kFmt, kQueries, D) | kBMajorMN;
-    const int lane = threadIdx.x & 31;
-    Cursor sc(p.w, B), pv(p.w, B);
+    const uint64_t k_desc = desc_k_sw128(k_smem), v_desc = desc_mn_sw128(v_smem, kPieceKeys * 128);
+    Cursor sc(p.w, B);
     uint32_t i = 0, runs = 0;                                  // tiles and runs scored
+    uint32_t fresh = 0;                                        // of the tiles scored ahead: bit set, the first of its run
     auto wait = [&](uint64_t &bar, uint32_t parity, unsigned what) {
-        if (mbar_wait_warp_fast(smem_u32(&bar), parity)) return true;
-        if (lane == 0) atomicOr(&g_status, what);
+        if (mbar_wait_fast(smem_u32(&bar), parity)) return true;
+        atomicOr(&g_status, what);
         return false;
     };
     auto score = [&] {
         if (!sc.more) return true;
         const int buf = i & 1;
-        if (sc.k == 0 && !wait(B.q_full, runs++ & 1, kErrTimeoutDrain)) return false;
+        if (sc.k == 0) {
+            if (!wait(B.q_full, runs++ & 1, kErrTimeoutDrain)) return false;
+            fresh |= 1u << buf;
+        } else {
+            fresh &= ~(1u << buf);
+        }
         if (!wait(B.k_full[buf], (i >> 1) & 1, kErrTimeoutLoad)) return false;
         tc_fence_after_sync();
-        if (elect_one()) {
-            const uint32_t kb = k_smem + buf * C::TileBytes;
+        const uint64_t kd = k_desc + buf * (C::KBytes >> 4);
 #pragma unroll
-            for (int part = 0; part < 2; ++part)               // the queries' high, then low parts
+        for (int part = 0; part < 3; ++part) {                 // Q_hi C_hi, Q_lo C_hi, Q_hi C_lo
+            const uint32_t q = tmem + C::QCol + (part == 1) * (D / 2), off = (part == 2) * C::TileBytes;
 #pragma unroll
-                for (int e = 0; e < D / 16; ++e)
-                    mma_f16_ts(tmem + buf * kTile, tmem + C::QCol + part * (D / 2) + e * 8,
-                               desc_k_sw128(kb + (e >> 2) * kTile * 128 + (e & 3) * 32), kIdS, part + e > 0);
-            mma_commit(smem_u32(&B.k_empty[buf]));
-            mma_commit(smem_u32(&B.s_full[buf]));
+            for (int e = 0; e < D / 16; ++e)
+                mma_f16_ts(tmem + buf * kTile, q + e * 8, kd + ((off + (e >> 2) * kTile * 128 + (e & 3) * 32) >> 4), kIdS,
+                           part + e > 0);
         }
+        mma_commit(smem_u32(&B.k_empty[buf]));
+        mma_commit(smem_u32(&B.s_full[buf]));
         ++i;
         sc.next();
         return true;
     };
     bool ok = score() && score();
-    for (uint32_t j = 0; ok && pv.more; ++j) {
-        const int buf = j & 1, s = j % C::VStages;
+    uint32_t stage = 0, phase = 0;
+    for (uint32_t j = 0; ok && j < i; ++j) {
+        const int buf = j & 1;
         if (!wait(B.p_full[buf], (j >> 1) & 1, kErrTimeoutDrain)) break;
-        if (!wait(B.v_full[s], (j / C::VStages) & 1, kErrTimeoutLoad)) break;
-        const int keys = pv.keys();
-        if (pv.r.seq >= 0 && keys < kTile) {
-            for (int e = 0; e < C::Blocks; ++e) {
-                uint4 *rows = reinterpret_cast<uint4 *>(v_ptr + s * C::TileBytes + e * kTile * 128);
-                for (int y = keys * 8 + lane; y < kTile * 8; y += 32) rows[y] = make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-        }
-        tc_fence_after_sync();
-        if (elect_one()) {
+        const bool first = (fresh >> buf) & 1;
 #pragma unroll
-            for (int e = 0; e < kTile / 16; ++e)
-                mma_f16_ts(tmem + C::OCol, tmem + buf * kTile + (e & 4) * 16 + (e & 3) * 8,   // each half's weights lie where its scores were
-                          
-                           desc_mn_sw128(v_smem + s * C::TileBytes + e * 2048, kTile * 128), kIdO, pv.k > 0 || e > 0);
-            mma_commit(smem_u32(&B.v_empty[s]));
-            mma_commit(smem_u32(&B.o_done));
+        for (int c = 0; c < 2 && ok; ++c) {
+            ok = wait(B.v_full[stage], phase, kErrTimeoutLoad);
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint64_t vd = v_desc + stage * (C::PieceBytes >> 4);
+#pragma unroll
+            for (int e = 0; e < kPieceKeys / 16; ++e)          // each half's weights lie where its scores were
+                mma_f16_ts(tmem + C::OCol, tmem + buf * kTile + c * 64 + e * 8, vd + (e * 2048 >> 4), kIdO,
+                           !first || c + e > 0);
+            mma_commit(smem_u32(&B.v_empty[stage]));
+            if (++stage == C::VStages) {
+                stage = 0;
+                phase ^= 1;
+            }
         }
-        pv.next();
+        if (!ok) break;
+        mma_commit(smem_u32(&B.o_done));
         ok = score();
     }
-    // all products complete before the tensor memory is freed
-    if (elect_one()) mma_commit(smem_u32(&B.drain));
+}
+
+template <int D, bool kBF16>
+__device__ void mma_role(const Params &p, Book &B, uint32_t k_smem, uint32_t v_smem, uint32_t tmem)
+{
+    if (elect_one()) {
+        issue_products<D, kBF16>(p, B, k_smem, v_smem, tmem);
+        mma_commit(smem_u32(&B.drain));                        // all products, before the tensor memory is freed
+    }
     __syncwarp();
     mbar_wait_warp(smem_u32(&B.drain), 0);
 }
 
+// Loads of V.  A tile that reaches behind its sequence's own keys is cleared there
+// before it is announced: those rows are weighed with 0, and may hold NaN.
 template <int D>
-__device__ void tma_role(const Params &p, Book &B, uint32_t v_smem)
+__device__ void tma_role(const Params &p, Book &B, uint8_t *v_ptr)
 {
     using C = Cfg<D>;
-    if ((threadIdx.x & 31) != 0) return;
-    uint32_t j = 0;
-    for (Cursor c(p.w, B); c.more; c.next(), ++j) {
-        const int s = j % C::VStages;
-        if (!mbar_wait(smem_u32(&B.v_empty[s]), ((j / C::VStages) & 1) ^ 1)) {
-            atomicOr(&g_status, kErrTimeoutMma);
+    const int lane = threadIdx.x & 31;
+    const uint32_t v_smem = smem_u32(v_ptr);
+    uint32_t j = 0, tails = 0;                                 // pieces loaded, tiles cleared
+    bool ok = true;
+    for (Cursor c(p.w, B); ok && c.more; c.next()) {
+        const bool own = c.r.seq >= 0;
+        const int keys = c.keys();
+        const bool tail = own && keys < kTile;
+        if (tail && lane == 0) mbar_arrive_expect_tx(smem_u32(&B.tail), 2 * C::PieceBytes);
+        for (int y = 0; y < 2; ++y, ++j) {
+            const int s = j % C::VStages;
+            if (!mbar_wait_warp(smem_u32(&B.v_empty[s]), ((j / C::VStages) & 1) ^ 1)) {
+                if (lane == 0) atomicOr(&g_status, kErrTimeoutMma);
+                ok = false;
+                break;
+            }
+            if (lane == 0) {
+                const uint32_t bar = smem_u32(tail ? &B.tail : &B.v_full[s]);
+                if (!tail) mbar_arrive_expect_tx(bar, C::PieceBytes);
+                for (int e = 0; e < C::Blocks; ++e)
+                    tma_load_3d(v_smem + s * C::PieceBytes + e * kPieceKeys * 128, own ? &p.own_v : &p.prefix_v, e * 64,
+                                c.tile() * kTile + y * kPieceKeys, own ? c.r.seg : c.r.head, bar);
+            }
+        }
+        if (!ok || !tail) continue;
+        if (!mbar_wait_warp_fast(smem_u32(&B.tail), tails++ & 1)) {
+            if (lane == 0) atomicOr(&g_status, kErrTimeoutLoad);
             break;
         }
-        const uint32_t bar = smem_u32(&B.v_full[s]);
-        mbar_arrive_expect_tx(bar, C::TileBytes);
-        const int z = c.r.seq >= 0 ? static_cast<int>(c.r.seg) : c.r.head;
-        for (int e = 0; e < C::Blocks; ++e)
-            tma_load_3d(v_smem + s * C::TileBytes + e * kTile * 128, c.r.seq >= 0 ? &p.own_v : &p.prefix_v, e * 64,
-                        c.tile() * kTile, z, bar);
+        for (int y = 0; y < 2; ++y) {
+            const int s = (j - 2 + y) % C::VStages, from = max(keys - y * kPieceKeys, 0);
+            for (int e = 0; e < C::Blocks; ++e) {
+                uint4 *rows = reinterpret_cast<uint4 *>(v_ptr + s * C::PieceBytes + e * kPieceKeys * 128);
+                for (int z = from * 8 + lane; z < kPieceKeys * 8; z += 32) rows[z] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&B.v_full[s]));
+        }
     }
-    for (uint32_t k = 0; k < C::VStages && k < j; ++k)         // every load lands before the CTA exits
-        mbar_wait(smem_u32(&B.v_full[(j - 1 - k) % C::VStages]), ((j - 1 - k) / C::VStages) & 1);
+    if (lane == 0)
+        for (uint32_t k = 0; k < C::VStages && k < j; ++k)     // every load lands before the CTA exits
+            mbar_wait(smem_u32(&B.v_full[(j - 1 - k) % C::VStages]), ((j - 1 - k) / C::VStages) & 1);
 }
 
 template <int D, int NB, bool kBF16>
 __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_constant__ Params p)
 {
     using C = Cfg<D>;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ Book B;
-    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    uint8_t *v_ptr = smem + C::KStages * C::TileBytes;
+    extern __shared__ __align__(1024) uint8_t smem[];          // centroids, values, bookkeeping
+    if ((smem_u32(smem) & 1023) != 0) {                        // the swizzled tiles need 1024-byte boundaries
+        if (threadIdx.x == 0) atomicOr(&g_status, kErrLayout);
+        return;
+    }
+    uint8_t *v_ptr = smem + C::KStages * C::KBytes;
+    Book &B = *reinterpret_cast<Book *>(v_ptr + C::VStages * C::PieceBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == kWarpTma && lane == 0) {
         for (int s = 0; s < C::VStages; ++s) {
@@ -545,6 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&B.n_full[s]), 4);
         mbar_init(smem_u32(&B.q_full), 8);
         mbar_init(smem_u32(&B.o_done), 1);
+        mbar_init(smem_u32(&B.tail), 1);
         mbar_init(smem_u32(&B.drain), 1);
         fence_mbar_init();
     }
@@ -566,8 +630,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     } else if (warp < kWarpMma) {
         code_role<D, NB>(p, B, (warp >> 2) & 1, smem);
     } else {
-        if (warp == kWarpMma) mma_role<D, kBF16>(p, B, v_ptr, smem_u32(smem), smem_u32(v_ptr), tmem);
-        else if (warp == kWarpTma) tma_role<D>(p, B, smem_u32(v_ptr));
+        if (warp == kWarpMma) mma_role<D, kBF16>(p, B, smem_u32(smem), smem_u32(v_ptr), tmem);
+        else if (warp == kWarpTma) tma_role<D>(p, B, v_ptr);
     }
     __syncwarp();
     tc_fence_before_sync();
@@ -576,33 +640,18 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     if (warp == kWarpMma) tmem_dealloc(tmem, 512);
 }
 
-// (heads, rows, d) dense values, box of 64 elements x 128 rows
+// (heads, rows, d) dense values, box of 64 elements x 64 rows
 bool make_map(CUtensorMap *map, const void *base, int dtype, int d, int64_t rows, int64_t heads)
 {
     if (rows == 0) return true;                                // never loaded from
     const EncodeTiledFn encode = encode_tiled();
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(heads)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(d) * 2 * rows};
-    const cuuint32_t box[3] = {64, kTile, 1}, es[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, kPieceKeys, 1}, es[3] = {1, 1, 1};
     return encode(map, dtype == AXR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                   const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// half_codebook of (d, b), kept
-HalfCodebook codebook_of(const Codebook &cb)
-{
-    static std::mutex mu;
-    static HalfCodebook kept[2][kMaxBits + 1];
-    static bool have[2][kMaxBits + 1];
-    std::lock_guard<std::mutex> lock(mu);
-    const int x = cb.d == 128;
-    if (!have[x][cb.b]) {
-        kept[x][cb.b] = half_codebook(cb.centroids, cb.d, cb.b);
-        have[x][cb.b] = true;
-    }
-    return kept[x][cb.b];
 }
 
 template <int D, int B, bool kBF16>
@@ -646,7 +695,7 @@ Work shared_tc_work(int batch, int heads, int group, int d)
     w.row_tiles = (rows + w.bm - 1) / w.bm;
     w.slot_rows = rows < w.bm ? rows : w.bm;
     w.ctas = device_sm_count();
-    w.min_tiles = 1;
+    w.run_cost = kRunCost;
     return w;
 }
 
@@ -661,12 +710,19 @@ cudaError_t launch_shared_main_tc(const SharedArgs &a, const Work &w, cudaStream
     p.idx = a.idx;
     p.prefix_norms = a.prefix_norms;
     p.norms = a.norms;
-    const HalfCodebook hc = codebook_of(a.cb);
-    p.inv_scale = 1.0f / hc.scale;
+    // the power of two that brings the centroids, near 1/sqrt(d), near 1
+    const float scale = a.d == 128 ? 16.0f : 8.0f;
+    p.inv_scale = 1.0f / scale;
     const int first = a.b == 4 ? 8 : 0, count = a.b == 4 ? 8 : 1 << a.b;
     for (int i = 0; i < count; ++i) {
-        p.lo[i / 4] |= static_cast<uint32_t>(hc.bits[first + i] & 0xff) << (8 * (i % 4));
-        p.hi[i / 4] |= static_cast<uint32_t>(hc.bits[first + i] >> 8) << (8 * (i % 4));
+        const float c = a.cb.centroids[first + i] * scale;
+        const __half hi = __float2half_rn(c);
+        const __half part[2] = {hi, __float2half_rn(c - __half2float(hi))};
+        for (int y = 0; y < 2; ++y) {
+            const uint32_t bits = __half_raw(part[y]).x;
+            p.table[y][0][i / 4] |= (bits & 0xffu) << (8 * (i % 4));
+            p.table[y][1][i / 4] |= (bits >> 8) << (8 * (i % 4));
+        }
     }
     AXR_DEBUG_ONLY(const uint64_t rows = static_cast<uint64_t>(a.heads) * a.n, pb = a.d * a.b / 8;
                    const uint64_t own = static_cast<uint64_t>(a.batch) * a.heads * a.capacity;
