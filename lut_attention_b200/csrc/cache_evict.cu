@@ -13,11 +13,14 @@
 // Eviction of head h with len rows, of which the last `recent` stay anyway:
 // among t < len - recent the k = keep - recent rows of largest weight stay,
 // equal weights by lowest t.  The weights become unsigned keys in the same order
-// and a radix search, 8 bits a round, finds the k-th largest: the head's cluster
-// counts its keys per digit in shared memory, the counts meet through distributed
-// shared memory, and the digit holding rank k is fixed.  Then one ordered pass
-// writes the slots that stay (all above the k-th key, and the first of those
-// equal to it), and a second kernel copies the rows.
+// and a radix search finds the k-th largest, a digit of 11 bits a round (the first
+// holds the sign, the exponent and 2 bits: 8 would put nearly all weights into two or
+// three counters): the head's cluster counts its keys per digit in shared memory, each
+// CTA adds up an eighth of the counters over the cluster for all of it (distributed
+// shared memory; adding to one CTA's counters took four times as long), and the digit
+// that holds rank k is fixed.  Then one ordered pass writes the slots that stay (all
+// above the k-th key, and the first of those equal to it), and a second kernel copies
+// the rows: it starts while the choice ends and is bound by the rows' bytes.
 #include <cooperative_groups.h>
 
 #include "axr_internal.cuh"
@@ -31,11 +34,12 @@ constexpr int kCluster = 8;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 
-// [begin, end) of CTA `rank`'s stretch of `count` elements
-__device__ __forceinline__ void stretch(int count, int rank, int &begin, int &end)
+// [begin, end) of CTA `rank`'s stretch of `count` elements, cut at multiples of 4
+__device__ __forceinline__ void stretch(int count, int rank, int ctas, int &begin, int &end)
 {
-    begin = static_cast<int>(static_cast<int64_t>(count) * rank / kCluster);
-    end = static_cast<int>(static_cast<int64_t>(count) * (rank + 1) / kCluster);
+    const int64_t fours = (static_cast<int64_t>(count) + 3) / 4;
+    begin = static_cast<int>(min(fours * rank / ctas * 4, static_cast<int64_t>(count)));
+    end = static_cast<int>(min(fours * (rank + 1) / ctas * 4, static_cast<int64_t>(count)));
 }
 
 struct WeightParams {
@@ -53,16 +57,39 @@ __device__ __forceinline__ int used_rows(const int32_t *lengths, int h, int most
     return min(max(len, 0), most);
 }
 
+// e^x for x <= 0: 2^(x log2 e) by the special function unit, within 2^-22 and the
+// rounding of the product, both relative (expf's exact reduction doubled the kernel's
+// instructions)
+__device__ __forceinline__ float exp_below(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    return y;
+}
+
 // (m, l) of two disjoint runs of keys; a NaN score makes l NaN
 __device__ __forceinline__ void join(float &m, float &l, float m2, float l2)
 {
     const float top = fmaxf(m, m2);
     const float base = top == -INFINITY ? 0.0f : top;
-    l = l * expf(m - base) + l2 * expf(m2 - base);
+    l = l * exp_below(m - base) + l2 * exp_below(m2 - base);
     m = top;
 }
 
-template <int G>
+// kVec consecutive floats at p (16-byte aligned when kVec = 4)
+template <int kVec>
+__device__ __forceinline__ void load_floats(const float *p, float (&v)[kVec])
+{
+    if constexpr (kVec == 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(p);
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    } else {
+        v[0] = *p;
+    }
+}
+
+// kVec = 4: rows and stretches start on 16-byte boundaries
+template <int G, int kVec>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) weights_kernel(const WeightParams p)
 {
     __shared__ float s_m[kWarps][G], s_l[kWarps][G];
@@ -72,8 +99,18 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) wei
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int len = used_rows(p.lengths, h, p.n AXR_DEBUG_ONLY(, p.sp_lengths));
     int t0, t1;
-    stretch(len, rank, t0, t1);
+    stretch(len, rank, kCluster, t0, t1);
     const float *src = p.scores + static_cast<int64_t>(h) * p.group * p.n;
+    // kVec scores of query g from key t on, -inf past the stretch
+    auto load = [&](int g, int t, float (&v)[kVec]) {
+        const float *at = src + static_cast<int64_t>(g) * p.n + t;
+        if (g < p.group && t + kVec <= t1 && AXR_IN(p.sp_scores, at, 4 * kVec)) {
+            load_floats<kVec>(at, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) v[e] = (g < p.group && t + e < t1 && AXR_IN(p.sp_scores, at + e, 4)) ? at[e] : -INFINITY;
+        }
+    };
 
     float m[G], l[G];
 #pragma unroll
@@ -81,25 +118,27 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) wei
         m[g] = -INFINITY;
         l[g] = 0.0f;
     }
-    constexpr int U = 4;
-    for (int t = t0 + threadIdx.x; t < t1; t += U * kThreads) {
-        float v[U][G];
+    // scores a thread has in flight: enough of them to cover the latency of the memory
+    constexpr int U = kVec == 4 ? (G <= 2 ? 4 : 2) : (G <= 4 ? 4 : 2);
+    for (int t = t0 + threadIdx.x * kVec; t < t1; t += U * kThreads * kVec) {
+        float v[U][G][kVec];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const float *at = src + static_cast<int64_t>(g) * p.n + t + u * kThreads;
-                v[u][g] = (g < p.group && t + u * kThreads < t1 && AXR_IN(p.sp_scores, at, 4)) ? *at : -INFINITY;
-            }
+            for (int g = 0; g < G; ++g) load(g, t + u * kThreads * kVec, v[u][g]);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             float top = m[g];
 #pragma unroll
-            for (int u = 0; u < U; ++u) top = fmaxf(top, v[u][g]);
-            const float base = top == -INFINITY ? 0.0f : top;
-            float sum = l[g] * expf(m[g] - base);
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int u = 0; u < U; ++u) sum += expf(v[u][g] - base);
+                for (int e = 0; e < kVec; ++e) top = fmaxf(top, v[u][g][e]);
+            const float base = top == -INFINITY ? 0.0f : top;
+            float sum = l[g] * exp_below(m[g] - base);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) sum += exp_below(v[u][g][e] - base);
             l[g] = sum;
             m[g] = top;
         }
@@ -126,21 +165,45 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) wei
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         float cm = -INFINITY, cl = 0.0f;
+#pragma unroll
         for (int r = 0; r < kCluster; ++r) join(cm, cl, *cluster.map_shared_rank(&c_m[g], r), *cluster.map_shared_rank(&c_l[g], r));
         base[g] = cm == -INFINITY ? 0.0f : cm;
         inv[g] = cl > 0.0f ? 1.0f / cl : cl;                  // a query without a key adds nothing, NaN stays NaN
     }
     cluster.sync();                                           // no CTA leaves while its (m, l) are read
     float *dst = p.weights + static_cast<int64_t>(h) * p.capacity;
-    for (int t = t0 + threadIdx.x; t < t1; t += kThreads) {
-        if (!AXR_IN(p.sp_weights, dst + t, 4)) continue;
-        float w = dst[t];
+    constexpr int U2 = U / 2;
+    for (int t = t0 + threadIdx.x * kVec; t < t1; t += U2 * kThreads * kVec) {
+        float v[U2][G][kVec], w[U2][kVec];
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const float *at = src + static_cast<int64_t>(g) * p.n + t;
-            if (g < p.group && AXR_IN(p.sp_scores, at, 4)) w = fmaf(expf(*at - base[g]), inv[g], w);
+        for (int u = 0; u < U2; ++u) {
+            const int at = t + u * kThreads * kVec;
+#pragma unroll
+            for (int g = 0; g < G; ++g) load(g, at, v[u][g]);
+            if (at + kVec <= t1 && AXR_IN(p.sp_weights, dst + at, 4 * kVec)) {
+                load_floats<kVec>(dst + at, w[u]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) w[u][e] = (at + e < t1 && AXR_IN(p.sp_weights, dst + at + e, 4)) ? dst[at + e] : 0.0f;
+            }
         }
-        dst[t] = w;
+#pragma unroll
+        for (int u = 0; u < U2; ++u) {
+            const int at = t + u * kThreads * kVec;
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                if (g < p.group) {
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) w[u][e] = fmaf(exp_below(v[u][g][e] - base[g]), inv[g], w[u][e]);
+                }
+            if (kVec == 4 && at + kVec <= t1 && AXR_IN(p.sp_weights, dst + at, 4 * kVec)) {
+                *reinterpret_cast<float4 *>(dst + at) = make_float4(w[u][0], w[u][kVec - 3], w[u][kVec - 2], w[u][kVec - 1]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e)
+                    if (at + e < t1 && AXR_IN(p.sp_weights, dst + at + e, 4)) dst[at + e] = w[u][e];
+            }
+        }
     }
 }
 
@@ -161,111 +224,143 @@ __device__ __forceinline__ uint32_t key_of(float w)
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) choose_kernel(const EvictParams p)
+constexpr int kHeldKeys = 24576;       // keys of a CTA's stretch that stay in shared memory (96 KB)
+
+// kCtas CTAs (one cluster) per head: one up to kOneCta rows, where exchanging counts
+// costs more than it saves, else kCluster
+constexpr int kOneCta = 8192;
+constexpr int kDigits = 3, kBins = 2048;   // digits of 11, 11 and 10 bits
+static_assert(kBins % kThreads == 0 && kWarps <= 32, "bins of a thread");
+template <int kCtas>
+__global__ void __launch_bounds__(kThreads, 2) choose_kernel(const EvictParams p)
 {
-    __shared__ int hist[256];                                 // read by the cluster
-    __shared__ int total[256];
-    __shared__ int s_above, s_equal;                          // this CTA's counts, read by the cluster
+    extern __shared__ uint32_t held[];                        // the stretch's keys, or as many as fit
+    __shared__ int hist[kBins];                               // read by the cluster
+    __shared__ int total[kBins];                              // the cluster's counts, written by the CTAs in parts
+    __shared__ int s_above[kCluster], s_equal[kCluster];      // by rank, written by that CTA
     __shared__ int s_digit, s_rank;
     __shared__ int warp_above[kWarps], warp_equal[kWarps];
     const cg::cluster_group cluster = cg::this_cluster();
-    const int h = blockIdx.x / kCluster, rank = static_cast<int>(cluster.block_rank());
+    const int h = blockIdx.x / kCtas, rank = kCtas == 1 ? 0 : static_cast<int>(cluster.block_rank());
+    auto sync_all = [&] {
+        if constexpr (kCtas == 1) __syncthreads();
+        else cluster.sync();
+    };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int len = used_rows(p.lengths, h, p.capacity AXR_DEBUG_ONLY(, p.sp_lengths));
     int *kept = p.kept + static_cast<int64_t>(h) * p.keep;
     auto put = [&](int at, int t) {
         if (AXR_IN(p.sp_kept, kept + at, 4)) kept[at] = t;
     };
+    // the copy may be scheduled; it waits for this kernel's end before it reads `kept`
+    asm volatile("griddepcontrol.launch_dependents;");
     if (rank == 0 && threadIdx.x == 0 && AXR_IN(p.sp_lengths_out, p.lengths_out + h, 4))
         p.lengths_out[h] = min(len, p.keep);
     if (len <= p.keep) {                                      // the whole cluster: all rows stay
-        for (int i = rank * kThreads + threadIdx.x; i < p.keep; i += kCluster * kThreads) put(i, i < len ? i : -1);
+        for (int i = rank * kThreads + threadIdx.x; i < p.keep; i += kCtas * kThreads) put(i, i < len ? i : -1);
         return;
     }
     const int old = len - p.recent, k = p.keep - p.recent;    // k of the first `old` rows stay, k < old
-    for (int i = rank * kThreads + threadIdx.x; i < p.recent; i += kCluster * kThreads) put(k + i, old + i);
+    for (int i = rank * kThreads + threadIdx.x; i < p.recent; i += kCtas * kThreads) put(k + i, old + i);
     if (k == 0) return;                                       // the whole cluster
     int t0, t1;
-    stretch(old, rank, t0, t1);
+    stretch(old, rank, kCtas, t0, t1);
     const float *src = p.weights + static_cast<int64_t>(h) * p.capacity;
-    auto key_at = [&](int t) { return AXR_IN(p.sp_weights, src + t, 4) ? key_of(__ldg(src + t)) : 0u; };
+    auto load_key = [&](int t) { return AXR_IN(p.sp_weights, src + t, 4) ? key_of(__ldg(src + t)) : 0u; };
+#pragma unroll 8
+    for (int t = t0 + threadIdx.x; t < min(t1, t0 + kHeldKeys); t += kThreads) held[t - t0] = load_key(t);
+    auto key_at = [&](int t) { return t - t0 < kHeldKeys ? held[t - t0] : load_key(t); };   // a thread reads back its own
+
+    for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0;
+    __syncthreads();
 
     uint32_t prefix = 0;                                      // the digits fixed so far
     int want = k;                                             // rank of the k-th largest among keys with that prefix
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = threadIdx.x; i < 256; i += kThreads) hist[i] = 0;
-        __syncthreads();
+#pragma unroll 1
+    for (int round = 0; round < kDigits; ++round) {
+        const int shift = round == 0 ? 21 : round == 1 ? 10 : 0, bits = round == 2 ? 10 : 11;
+        const uint32_t mask = (1u << bits) - 1u;
         for (int t = t0 + threadIdx.x; t < t1; t += kThreads) {
             const uint32_t key = key_at(t);
-            if (shift == 24 || (key >> (shift + 8)) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1);
+            if (round == 0 || (key >> (shift + bits)) == prefix) atomicAdd(&hist[(key >> shift) & mask], 1);
         }
-        cluster.sync();
-        if (threadIdx.x < 256) {
-            int sum = 0;
-            for (int r = 0; r < kCluster; ++r) sum += cluster.map_shared_rank(hist, r)[threadIdx.x];
-            total[threadIdx.x] = sum;
+        sync_all();
+        const int *sums = kCtas == 1 ? hist : total;
+        if constexpr (kCtas > 1) {                            // this CTA adds up its part of the bins for all
+            constexpr int kPart = kBins / kCluster;
+            for (int i = rank * kPart + threadIdx.x; i < (rank + 1) * kPart; i += kThreads) {
+                int sum = 0;
+#pragma unroll
+                for (int r = 0; r < kCluster; ++r) sum += cluster.map_shared_rank(hist, r)[i];
+#pragma unroll
+                for (int r = 0; r < kCluster; ++r) cluster.map_shared_rank(total, r)[i] = sum;
+            }
+            cluster.sync();
         }
-        cluster.sync();                                       // total is whole; no CTA clears counts that are read
-        if (warp == 0) {                                      // the digit where the count from above reaches `want`
-            int own[8], sum = 0;
+        // the digit where the count from above reaches `want`: a thread has kBins /
+        // kThreads neighbouring bins, thread 0 the highest
+        constexpr int kOwn = kBins / kThreads;
+        int own[kOwn], sum = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                own[i] = total[255 - (lane * 8 + i)];
-                sum += own[i];
-            }
-            int upto = sum;
+        for (int i = 0; i < kOwn; ++i) {
+            own[i] = sums[kBins - 1 - (threadIdx.x * kOwn + i)];
+            sum += own[i];
+        }
+        int upto = sum;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += x;
-            }
-            int before = upto - sum;
-            if (before < want && want <= upto) {
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        if (lane == 31) warp_above[warp] = upto;
+        __syncthreads();
+        int before = upto - sum + __reduce_add_sync(0xffffffffu, lane < warp ? warp_above[lane & (kWarps - 1)] : 0);
+        if (before < want && want <= before + sum) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (before < want && want <= before + own[i]) {
-                        s_digit = 255 - (lane * 8 + i);
-                        s_rank = want - before;
-                    }
-                    before += own[i];
+            for (int i = 0; i < kOwn; ++i) {
+                if (before < want && want <= before + own[i]) {
+                    s_digit = kBins - 1 - (threadIdx.x * kOwn + i);
+                    s_rank = want - before;
                 }
+                before += own[i];
             }
         }
         __syncthreads();
-        prefix = (prefix << 8) | static_cast<uint32_t>(s_digit);
+        prefix = (prefix << bits) | static_cast<uint32_t>(s_digit);
         want = s_rank;
+        for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0;
         __syncthreads();
     }
     // keys above `prefix` stay, and of those equal to it the first `want`
-    int above = 0, equal = 0;
-    for (int t = t0 + threadIdx.x; t < t1; t += kThreads) {
-        const uint32_t key = key_at(t);
-        above += key > prefix;
-        equal += key == prefix;
-    }
-    above = __reduce_add_sync(0xffffffffu, above);
-    equal = __reduce_add_sync(0xffffffffu, equal);
-    if (lane == 0) {
-        warp_above[warp] = above;
-        warp_equal[warp] = equal;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        int a = 0, e = 0;
-        for (int i = 0; i < kWarps; ++i) {
-            a += warp_above[i];
-            e += warp_equal[i];
-        }
-        s_above = a;
-        s_equal = e;
-    }
-    cluster.sync();
     int above_before = 0, equal_before = 0;
-    for (int r = 0; r < rank; ++r) {
-        above_before += *cluster.map_shared_rank(&s_above, r);
-        equal_before += *cluster.map_shared_rank(&s_equal, r);
+    if constexpr (kCtas > 1) {                                // how many of either the CTAs before this one have
+        int above = 0, equal = 0;
+        for (int t = t0 + threadIdx.x; t < t1; t += kThreads) {
+            const uint32_t key = key_at(t);
+            above += key > prefix;
+            equal += key == prefix;
+        }
+        above = __reduce_add_sync(0xffffffffu, above);
+        equal = __reduce_add_sync(0xffffffffu, equal);
+        if (lane == 0) {
+            warp_above[warp] = above;
+            warp_equal[warp] = equal;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            const int a = __reduce_add_sync(0xffffffffu, lane < kWarps ? warp_above[lane] : 0);
+            const int e = __reduce_add_sync(0xffffffffu, lane < kWarps ? warp_equal[lane] : 0);
+            if (lane < kCluster) {                            // to every CTA of the cluster
+                cluster.map_shared_rank(s_above, lane)[rank] = a;
+                cluster.map_shared_rank(s_equal, lane)[rank] = e;
+            }
+        }
+        cluster.sync();                                       // the last access to another CTA's memory
+        for (int r = 0; r < rank; ++r) {
+            above_before += s_above[r];
+            equal_before += s_equal[r];
+        }
     }
-    cluster.sync();                                           // no CTA leaves while its counts are read
     for (int base = t0; base < t1; base += kThreads) {        // in order, kThreads rows at a time
         const int t = base + threadIdx.x;
         const uint32_t key = t < t1 ? key_at(t) : 0u;
@@ -276,22 +371,15 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) cho
             warp_equal[warp] = __popc(be);
         }
         __syncthreads();
-        int a = above_before, e = equal_before, all_a = above_before, all_e = equal_before;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            if (i < warp) {
-                a += warp_above[i];
-                e += warp_equal[i];
-            }
-            all_a += warp_above[i];
-            all_e += warp_equal[i];
-        }
+        // every warp scans the warps' counts itself
+        const int wa = lane < kWarps ? warp_above[lane] : 0, we = lane < kWarps ? warp_equal[lane] : 0;
+        const bool before = lane < warp;
         const unsigned lower = (1u << lane) - 1u;
-        a += __popc(ba & lower);
-        e += __popc(be & lower);
+        const int a = above_before + __reduce_add_sync(0xffffffffu, before ? wa : 0) + __popc(ba & lower);
+        const int e = equal_before + __reduce_add_sync(0xffffffffu, before ? we : 0) + __popc(be & lower);
         if (is_above || (is_equal && e < want)) put(a + min(e, want), t);
-        above_before = all_a;
-        equal_before = all_e;
+        above_before += __reduce_add_sync(0xffffffffu, wa);
+        equal_before += __reduce_add_sync(0xffffffffu, we);
         __syncthreads();
     }
 }
@@ -308,7 +396,7 @@ struct CopyParams {
     AXR_DEBUG_ONLY(dbg::Span sp_kept, sp_idx, sp_V, sp_norms, sp_weights, sp_idx_out, sp_V_out, sp_norms_out, sp_weights_out;)
 };
 
-constexpr int kCopyRows = 32;          // rows of a CTA
+constexpr int kCopyRows = 64;          // rows of a CTA
 constexpr int kCopyThreads = 256;
 
 // CTA: kCopyRows rows of one head; a value row is v_bytes / 16 pieces, a packed
@@ -317,6 +405,7 @@ template <typename U>
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p)
 {
     __shared__ int s_from[kCopyRows];
+    asm volatile("griddepcontrol.wait;" ::: "memory");        // `kept` is written
     const int h = blockIdx.y, i0 = blockIdx.x * kCopyRows;
     const int rows = min(kCopyRows, p.keep - i0);
     const int64_t from0 = static_cast<int64_t>(h) * p.capacity, to0 = static_cast<int64_t>(h) * p.capacity_out + i0;
@@ -332,22 +421,100 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p)
         }
     }
     __syncthreads();
-    const int vp = p.v_bytes / 16;
-    for (int c = threadIdx.x; c < rows * vp; c += kCopyThreads) {
-        const int i = c / vp, e = c % vp;
-        if (s_from[i] < 0) continue;
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.V + (from0 + s_from[i]) * p.v_bytes) + e;
-        uint4 *dst = reinterpret_cast<uint4 *>(p.V_out + (to0 + i) * p.v_bytes) + e;
-        if (AXR_IN(p.sp_V, src, 16) && AXR_IN(p.sp_V_out, dst, 16)) *dst = __ldcs(src);
-    }
-    const int pp = p.p_bytes / static_cast<int>(sizeof(U));
-    for (int c = threadIdx.x; c < rows * pp; c += kCopyThreads) {
-        const int i = c / pp, e = c % pp;
-        if (s_from[i] < 0) continue;
-        const U *src = reinterpret_cast<const U *>(p.idx + (from0 + s_from[i]) * p.p_bytes) + e;
-        U *dst = reinterpret_cast<U *>(p.idx_out + (to0 + i) * p.p_bytes) + e;
-        if (AXR_IN(p.sp_idx, src, sizeof(U)) && AXR_IN(p.sp_idx_out, dst, sizeof(U))) *dst = __ldcs(src);
-    }
+    // kInFlight pieces of a thread are loaded before the first is stored
+    auto copy = [&](auto unit, const char *src, char *dst, int bytes AXR_DEBUG_ONLY(, const dbg::Span &sp, const dbg::Span &sp_out)) {
+        using U_ = decltype(unit);
+        constexpr int kInFlight = 4;
+        const int per = bytes / static_cast<int>(sizeof(U_)), pieces = rows * per;
+        for (int c0 = threadIdx.x; c0 < pieces; c0 += kInFlight * kCopyThreads) {
+            U_ v[kInFlight];
+#pragma unroll
+            for (int y = 0; y < kInFlight; ++y) {
+                const int c = c0 + y * kCopyThreads, i = c / per;
+                if (c >= pieces || s_from[i] < 0) continue;
+                const U_ *at = reinterpret_cast<const U_ *>(src + (from0 + s_from[i]) * bytes) + (c - i * per);
+                if (AXR_IN(sp, at, sizeof(U_))) v[y] = __ldcs(at);
+            }
+#pragma unroll
+            for (int y = 0; y < kInFlight; ++y) {
+                const int c = c0 + y * kCopyThreads, i = c / per;
+                if (c >= pieces || s_from[i] < 0) continue;
+                U_ *to = reinterpret_cast<U_ *>(dst + (to0 + i) * bytes) + (c - i * per);
+                if (AXR_IN(sp_out, to, sizeof(U_))) *to = v[y];
+            }
+        }
+    };
+    copy(uint4{}, p.V, p.V_out, p.v_bytes AXR_DEBUG_ONLY(, p.sp_V, p.sp_V_out));
+    copy(U{}, p.idx, p.idx_out, p.p_bytes AXR_DEBUG_ONLY(, p.sp_idx, p.sp_idx_out));
+}
+
+}  // namespace
+
+namespace {
+
+template <int kVec>
+void launch_weights(const WeightParams &p, unsigned grid, cudaStream_t stream)
+{
+    if (p.group <= 1) weights_kernel<1, kVec><<<grid, kThreads, 0, stream>>>(p);
+    else if (p.group <= 2) weights_kernel<2, kVec><<<grid, kThreads, 0, stream>>>(p);
+    else if (p.group <= 4) weights_kernel<4, kVec><<<grid, kThreads, 0, stream>>>(p);
+    else weights_kernel<8, kVec><<<grid, kThreads, 0, stream>>>(p);
+}
+
+// launch of `kernel` on `grid` CTAs in clusters of `ctas`
+template <typename P>
+cudaError_t launch_clusters(void (*kernel)(P), const P &p, unsigned grid, unsigned ctas, unsigned threads, size_t smem,
+                            cudaStream_t stream)
+{
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = ctas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// launch whose start may overlap the end of the kernel before it (it waits for that
+// kernel's results itself)
+template <typename P>
+cudaError_t launch_after(void (*kernel)(P), const P &p, dim3 grid, unsigned threads, cudaStream_t stream)
+{
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
+namespace {
+
+// The choice's shared-memory limit, and as large a share of the SM for it: by default
+// the driver set aside room for one CTA per SM, and the clusters ran in two waves.
+template <int kCtas>
+cudaError_t allow_choose()
+{
+    static std::atomic<unsigned long long> done{0}, carved{0};
+    const void *kernel = reinterpret_cast<const void *>(&choose_kernel<kCtas>);
+    cudaError_t e = allow_dynamic_smem(kernel, 4 * kHeldKeys, done);
+    int dev = 0;
+    if (e == cudaSuccess) e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (carved.load() >> dev & 1))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess && dev < 64) carved.fetch_or(1ull << dev);
+    return e;
 }
 
 }  // namespace
@@ -365,10 +532,10 @@ cudaError_t launch_accumulate_weights(const WeightArgs &a, cudaStream_t stream)
                    p.sp_weights = dbg::span(a.weights, 4ull * a.heads * a.capacity);
                    p.sp_lengths = dbg::span(a.lengths, a.lengths ? 4ull * a.heads : 0);)
     const unsigned grid = static_cast<unsigned>(a.heads) * kCluster;
-    if (a.group <= 1) weights_kernel<1><<<grid, kThreads, 0, stream>>>(p);
-    else if (a.group <= 2) weights_kernel<2><<<grid, kThreads, 0, stream>>>(p);
-    else if (a.group <= 4) weights_kernel<4><<<grid, kThreads, 0, stream>>>(p);
-    else weights_kernel<8><<<grid, kThreads, 0, stream>>>(p);
+    const bool aligned = a.n % 4 == 0 && a.capacity % 4 == 0 &&
+                         ((reinterpret_cast<uintptr_t>(a.scores) | reinterpret_cast<uintptr_t>(a.weights)) & 15) == 0;
+    if (aligned) launch_weights<4>(p, grid, stream);
+    else launch_weights<1>(p, grid, stream);
     return cudaGetLastError();
 }
 
@@ -386,8 +553,13 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream)
                    p.sp_lengths = dbg::span(a.lengths, 4ull * a.heads);
                    p.sp_kept = dbg::span(a.kept, 4ull * a.heads * a.keep);
                    p.sp_lengths_out = dbg::span(a.lengths_out, 4ull * a.heads);)
-    choose_kernel<<<static_cast<unsigned>(a.heads) * kCluster, kThreads, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
+    const bool one = a.capacity <= kOneCta;
+    const int64_t keys = one ? a.capacity : (a.capacity + kCluster - 1) / kCluster + 4;   // of a stretch at most
+    const size_t smem = 4 * static_cast<size_t>(keys < kHeldKeys ? keys : kHeldKeys);
+    cudaError_t e = one ? allow_choose<1>() : allow_choose<kCluster>();
+    if (e != cudaSuccess) return e;
+    if (one) e = launch_clusters(&choose_kernel<1>, p, static_cast<unsigned>(a.heads), 1, kThreads, smem, stream);
+    else e = launch_clusters(&choose_kernel<kCluster>, p, static_cast<unsigned>(a.heads) * kCluster, kCluster, kThreads, smem, stream);
     if (e != cudaSuccess) return e;
     CopyParams c{};
     c.kept = a.kept;
@@ -414,10 +586,9 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream)
                    c.sp_norms_out = dbg::span(a.norms_out, rows_out * 4);
                    c.sp_weights_out = dbg::span(a.weights_out, rows_out * 4);)
     const dim3 grid((p.keep + kCopyRows - 1) / kCopyRows, a.heads);
-    if (c.p_bytes % 16 == 0) copy_kernel<uint4><<<grid, kCopyThreads, 0, stream>>>(c);
-    else if (c.p_bytes % 4 == 0) copy_kernel<uint32_t><<<grid, kCopyThreads, 0, stream>>>(c);
-    else copy_kernel<uint8_t><<<grid, kCopyThreads, 0, stream>>>(c);
-    return cudaGetLastError();
+    if (c.p_bytes % 16 == 0) return launch_after(&copy_kernel<uint4>, c, grid, kCopyThreads, stream);
+    if (c.p_bytes % 4 == 0) return launch_after(&copy_kernel<uint32_t>, c, grid, kCopyThreads, stream);
+    return launch_after(&copy_kernel<uint8_t>, c, grid, kCopyThreads, stream);
 }
 
 }  // namespace axr

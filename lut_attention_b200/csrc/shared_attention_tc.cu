@@ -50,9 +50,11 @@ constexpr int kQueries = 128;
 constexpr int kPieceKeys = 64;                 // values come in pieces of half a tile
 constexpr int kCodeWarps = 8;                  // after the eight of the softmax
 constexpr int kWarpMma = 8 + kCodeWarps, kWarpTma = kWarpMma + 1;
-constexpr int kThreads = (kWarpTma + 1) * 32;
+constexpr int kThreads = 640;                  // two idle warps fill the fifth warpgroup
+// shares of the 96 registers a thread that 640 threads get at launch
+constexpr int kSoftmaxRegs = 136, kCodeRegs = 72, kOtherRegs = 64;
+static_assert(2 * kSoftmaxRegs + 2 * kCodeRegs + kOtherRegs <= 5 * 96, "registers of the block");
 constexpr int kRunCost = 3;                    // a run's queries and sums, in tiles
-constexpr int kPolyShare = 2;                  // of 8 pairs of exponentials on the FMA pipes
 constexpr int kIndexed = 256;                  // sequences whose starts and lengths fit shared memory
 
 __device__ unsigned int g_status;
@@ -231,11 +233,10 @@ __device__ void softmax_role(const Params &p, Book &B, int half, uint32_t tmem)
                     }
                     tmem_wait_st();
                 }
-                uint32_t s[32];
-                scaled32(s_half + 32, norms + 32, s);
-                float mx = max32(s, -INFINITY);
-                scaled32(s_half, norms, s);                    // kept for the weights
-                mx = max32(s, mx);
+                uint32_t s0[32], s1[32];
+                scaled32(s_half, norms, s0);
+                scaled32(s_half + 32, norms + 32, s1);
+                float mx = max32(s1, max32(s0, -INFINITY));
                 float(*word)[kQueries] = B.word[i & 1];
                 word[half][row] = mx;
                 meet_partner(meet_id);
@@ -263,15 +264,14 @@ __device__ void softmax_role(const Params &p, Book &B, int half, uint32_t tmem)
                 const uint64_t scale2 = pair(rs, rs), c2 = pair(c0, c0);
                 uint64_t sum0 = pair(l, 0.0f), sum1 = pair(0.0f, 0.0f);
                 uint32_t w[16];
-                weights32<kBF16, kPolyShare>(s, scale2, c2, sum0, sum1, w);
-                scaled32(s_half + 32, norms + 32, s);
+                weights32<kBF16, 0>(s0, scale2, c2, sum0, sum1, w);
                 tmem_st16(s_half, w);                          // over scores that are read already
-                weights32<kBF16, kPolyShare>(s, scale2, c2, sum0, sum1, w);
+                weights32<kBF16, 0>(s1, scale2, c2, sum0, sum1, w);
                 tmem_st16(s_half + 16, w);
-                float s0, s1, s2, s3;
-                unpair(sum0, s0, s1);
-                unpair(sum1, s2, s3);
-                l = (s0 + s1) + (s2 + s3);
+                float l0, l1, l2, l3;
+                unpair(sum0, l0, l1);
+                unpair(sum1, l2, l3);
+                l = (l0 + l1) + (l2 + l3);
                 tmem_wait_st();
                 tc_fence_before_sync();
                 // A wait tells a phase only from its neighbours, and the last two P V could
@@ -626,10 +626,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     tc_fence_after_sync();
     const uint32_t tmem = B.tmem_base;
     if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         softmax_role<D, kBF16>(p, B, warp >> 2, tmem);
     } else if (warp < kWarpMma) {
+        if constexpr (kCodeRegs < 96) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCodeRegs));
         code_role<D, NB>(p, B, (warp >> 2) & 1, smem);
     } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kWarpMma) mma_role<D, kBF16>(p, B, smem_u32(smem), smem_u32(v_ptr), tmem);
         else if (warp == kWarpTma) tma_role<D>(p, B, v_ptr);
     }
