@@ -8,6 +8,7 @@ There is no CPU path: without the built library or a CUDA device the calls raise
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -64,6 +65,8 @@ class AxrError(RuntimeError):
 def library() -> ctypes.CDLL:
     """Load libaxr.so (built in-tree by ``python -m lut_attention_b200.build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -96,8 +99,11 @@ def _call(name: str, device: torch.device, stream, *args) -> None:
     """Call libaxr's `name` with the tensors' device current (the library checks its
     pointers against, and launches on, the current device), on `stream` or that
     device's current stream; a status other than AXR_OK raises."""
-    with torch.cuda.device(device):
-        rc = getattr(library(), name)(*args, _stream_handle(stream, device))
+    if device.type == "cuda" and device.index == torch.cuda.current_device():
+        rc = getattr(library(), name)(*args, _stream_handle(stream, device))     # spares the switch there and back
+    else:
+        with torch.cuda.device(device):
+            rc = getattr(library(), name)(*args, _stream_handle(stream, device))
     _raise(rc, name)
 
 
@@ -481,6 +487,12 @@ def axr_attention_shared_workspace_bytes(batch: int, heads: int, group: int, d: 
     return out.value
 
 
+@functools.lru_cache(maxsize=256)
+def _shared_workspace_bytes(batch: int, heads: int, group: int, d: int, device: torch.device) -> int:
+    with torch.cuda.device(device):
+        return axr_attention_shared_workspace_bytes(batch, heads, group, d)
+
+
 def axr_attention_shared(q: torch.Tensor, prefix_idx: torch.Tensor, prefix_norms: torch.Tensor,
                          prefix_V: torch.Tensor, idx: torch.Tensor, norms: torch.Tensor, V: torch.Tensor,
                          lengths: torch.Tensor, group: int, b: int, signs: torch.Tensor,
@@ -521,8 +533,7 @@ def axr_attention_shared(q: torch.Tensor, prefix_idx: torch.Tensor, prefix_norms
     if lse is None:
         lse = torch.empty(rows, dtype=torch.float32, device=q.device)
     if workspace is None:
-        with torch.cuda.device(q.device):
-            need = axr_attention_shared_workspace_bytes(batch, heads, group, d)
+        need = _shared_workspace_bytes(batch, heads, group, d, q.device)
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     for t, name in ((out, "out"), (lse, "lse"), (workspace, "workspace")):
         _require_cuda(t, name)

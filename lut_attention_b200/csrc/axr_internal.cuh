@@ -211,4 +211,27 @@ EncodeTiledFn encode_tiled();
 // up are set on every call).  Safe to call from several host threads.
 cudaError_t allow_dynamic_smem(const void *kernel, size_t bytes, std::atomic<unsigned long long> &done);
 
+// Launch of a kernel that may start while the one before it on the stream ends: it
+// sets itself up and then waits (griddepcontrol.wait) for that kernel's results.
+template <typename P>
+cudaError_t launch_following(void (*kernel)(const P), const P &p, dim3 grid, unsigned threads, size_t smem, cudaStream_t stream)
+{
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void let_following_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+#endif
+
 }  // namespace axr

@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 2) choose_kernel(const EvictParams p
         if (AXR_IN(p.sp_kept, kept + at, 4)) kept[at] = t;
     };
     // the copy may be scheduled; it waits for this kernel's end before it reads `kept`
-    asm volatile("griddepcontrol.launch_dependents;");
+    let_following_start();
     if (rank == 0 && threadIdx.x == 0 && AXR_IN(p.sp_lengths_out, p.lengths_out + h, 4))
         p.lengths_out[h] = min(len, p.keep);
     if (len <= p.keep) {                                      // the whole cluster: all rows stay
@@ -405,7 +405,7 @@ template <typename U>
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p)
 {
     __shared__ int s_from[kCopyRows];
-    asm volatile("griddepcontrol.wait;" ::: "memory");        // `kept` is written
+    wait_for_previous();                                      // `kept` is written
     const int h = blockIdx.y, i0 = blockIdx.x * kCopyRows;
     const int rows = min(kCopyRows, p.keep - i0);
     const int64_t from0 = static_cast<int64_t>(h) * p.capacity, to0 = static_cast<int64_t>(h) * p.capacity_out + i0;
@@ -474,23 +474,6 @@ cudaError_t launch_clusters(void (*kernel)(P), const P &p, unsigned grid, unsign
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
-// launch whose start may overlap the end of the kernel before it (it waits for that
-// kernel's results itself)
-template <typename P>
-cudaError_t launch_after(void (*kernel)(P), const P &p, dim3 grid, unsigned threads, cudaStream_t stream)
-{
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
@@ -586,9 +569,9 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t stream)
                    c.sp_norms_out = dbg::span(a.norms_out, rows_out * 4);
                    c.sp_weights_out = dbg::span(a.weights_out, rows_out * 4);)
     const dim3 grid((p.keep + kCopyRows - 1) / kCopyRows, a.heads);
-    if (c.p_bytes % 16 == 0) return launch_after(&copy_kernel<uint4>, c, grid, kCopyThreads, stream);
-    if (c.p_bytes % 4 == 0) return launch_after(&copy_kernel<uint32_t>, c, grid, kCopyThreads, stream);
-    return launch_after(&copy_kernel<uint8_t>, c, grid, kCopyThreads, stream);
+    if (c.p_bytes % 16 == 0) return launch_following(&copy_kernel<uint4>, c, grid, kCopyThreads, 0, stream);
+    if (c.p_bytes % 4 == 0) return launch_following(&copy_kernel<uint32_t>, c, grid, kCopyThreads, 0, stream);
+    return launch_following(&copy_kernel<uint8_t>, c, grid, kCopyThreads, 0, stream);
 }
 
 }  // namespace axr

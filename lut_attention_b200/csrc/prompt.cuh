@@ -40,13 +40,15 @@ inline int prompt_tiles(const PromptShape &s, int bm)
     return static_cast<int>(full + ragged);
 }
 
-// The tile of BM queries that comes `index`-th over all sequences, the last
-// tiles of a sequence first (they see the most keys, so the grid's tail is its
-// short ones); false past the last.  Called by whole warps with the same index.
+// The tile of BM queries that comes `index`-th over all sequences; false past the
+// last.  Tiles that see more keys come first, so that those dealt last are short: by
+// their place in the sequence, from the last down, for up to 32 sequences (one lane
+// each); for more, sequence by sequence.  Called by whole warps with the same index.
 template <int BM>
 __device__ __forceinline__ bool find_tile(const PromptShape &s, int index,
                                           PromptTile &t AXR_DEBUG_ONLY(, const dbg::Span &sp_q, const dbg::Span &sp_k))
 {
+    constexpr unsigned kAll = 0xffffffffu;
     const int lane = threadIdx.x & 31;
     auto start = [&](const int32_t *cu, int i, int total AXR_DEBUG_ONLY(, const dbg::Span &sp)) {
         const int v = AXR_IN(sp, cu + i, 4) ? cu[i] : 0;
@@ -60,25 +62,43 @@ __device__ __forceinline__ bool find_tile(const PromptShape &s, int index,
             len = max(0, start(s.cu_q, b + 1, s.total_q AXR_DEBUG_ONLY(, sp_q)) - first);
         }
         const int tiles = (len + BM - 1) / BM;
-        int upto = tiles;                                     // inclusive scan over the warp
+        int src, place;                                       // the sequence's lane and the tile's place in it
+        if (s.batch <= 32) {
+            // above(r): tiles at place r or later, which come before those at r - 1
+            auto above = [&](int r) { return static_cast<int>(__reduce_add_sync(kAll, static_cast<unsigned>(max(tiles - r, 0)))); };
+            if (index >= above(0)) return false;
+            int lo = 0, hi = static_cast<int>(__reduce_max_sync(kAll, static_cast<unsigned>(tiles)));
+            while (hi - lo > 1) {                             // above(lo) > index >= above(hi)
+                const int mid = (lo + hi) >> 1;
+                if (above(mid) > index) lo = mid;
+                else hi = mid;
+            }
+            place = lo;
+            unsigned left = __ballot_sync(kAll, tiles > place);
+            for (int k = index - above(place + 1); k > 0; --k) left &= left - 1;
+            src = __ffs(left) - 1;
+        } else {
+            int upto = tiles;                                 // inclusive scan over the warp
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += x;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(kAll, upto, o);
+                if (lane >= o) upto += x;
+            }
+            const unsigned hit = __ballot_sync(kAll, index < upto);
+            if (!hit) {
+                index -= __shfl_sync(kAll, upto, 31);
+                continue;
+            }
+            src = __ffs(hit) - 1;
+            const int before = __shfl_sync(kAll, upto - tiles, src);
+            place = __shfl_sync(kAll, tiles, src) - 1 - (index - before);
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, index < upto);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            const int before = __shfl_sync(0xffffffffu, upto - tiles, src);
-            const int n = __shfl_sync(0xffffffffu, tiles, src);
-            t.first_q = __shfl_sync(0xffffffffu, first, src);
-            t.len_q = __shfl_sync(0xffffffffu, len, src);
-            t.row = (n - 1 - (index - before)) * BM;
-            t.first_k = start(s.cu_k, b0 + src, s.total_k AXR_DEBUG_ONLY(, sp_k));
-            t.len_k = max(0, start(s.cu_k, b0 + src + 1, s.total_k AXR_DEBUG_ONLY(, sp_k)) - t.first_k);
-            return true;
-        }
-        index -= __shfl_sync(0xffffffffu, upto, 31);
+        t.first_q = __shfl_sync(kAll, first, src);
+        t.len_q = __shfl_sync(kAll, len, src);
+        t.row = place * BM;
+        t.first_k = start(s.cu_k, b0 + src, s.total_k AXR_DEBUG_ONLY(, sp_k));
+        t.len_k = max(0, start(s.cu_k, b0 + src + 1, s.total_k AXR_DEBUG_ONLY(, sp_k)) - t.first_k);
+        return true;
     }
     return false;
 }

@@ -19,9 +19,10 @@
 // K and V pass through a ring of 32 KB (d = 64: 16 KB) pieces: a tile of K or V, at
 // d = 256 half of one (128 dimensions of K, 64 keys of V).
 //
-// Work items are (tile of queries, query head), dealt round-robin with the tiles
-// that see most keys first.  The next item's loads and first products run under
-// the epilogue of this one.
+// Work items are (tile of queries, query head), those that see most keys first,
+// dealt to the CTAs in turns whose direction alternates, so that the CTA that took
+// the largest item of one turn takes the smallest of the next.  The next item's
+// loads and first products run under the epilogue of this one.
 //
 // Every wait is bounded (sm100.cuh); a wait that runs out records a status bit
 // and ends its role.
@@ -99,6 +100,13 @@ struct Item {
     int most;                  // tiles of keys loaded
 };
 
+// the item that this CTA takes in a turn
+__device__ __forceinline__ int64_t item_of(int turn)
+{
+    const int at = turn & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+    return static_cast<int64_t>(turn) * gridDim.x + at;
+}
+
 template <int D>
 __device__ __forceinline__ bool item_at(const Params &p, int64_t i, Item &x)
 {
@@ -140,7 +148,9 @@ __device__ void softmax_role(const Params &p, Book &B, int t, int half, uint32_t
         }
     };
     uint32_t count = 0;                                        // tiles so far: phases of s_full and o_done
-    for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+    for (int turn = 0;; ++turn) {
+        const int64_t i = item_of(turn);
+        if (i >= items) break;
         Item x;
         if (!item_at<D>(p, i, x)) break;
         const int rows = t == 0 ? x.rows[0] : x.rows[1], n = t == 0 ? x.n[0] : x.n[1];
@@ -282,7 +292,9 @@ __device__ void tma_role(const Params &p, Book &B, uint8_t *ring_ptr, uint32_t q
         ++pieces;
         return true;
     };
-    for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+    for (int turn = 0;; ++turn) {
+        const int64_t i = item_of(turn);
+        if (i >= items) break;
         Item x;
         if (!item_at<D>(p, i, x)) break;
         if (lane == 0 && ok) {
@@ -538,7 +550,9 @@ __device__ void mma_role(const Params &p, Book &B, uint32_t q_smem, uint32_t rin
     using C = Cfg<D>;
     const int64_t items = static_cast<int64_t>(p.tiles) * p.s.heads * p.s.group;
     Products<D, kBF16> x(B, q_smem, ring, tmem);
-    for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+    for (int turn = 0;; ++turn) {
+        const int64_t i = item_of(turn);
+        if (i >= items) break;
         Item it;
         if (!item_at<D>(p, i, it)) break;
         bool ok = true;

@@ -72,8 +72,8 @@ __device__ __forceinline__ Line line_of(const Work &w, int own)
     x.prefix_places = places(w, w.n);
     x.own_first = w.heads * w.row_tiles * x.prefix_places;
     x.total = x.own_first + w.heads * own;
-    // no stretch shorter than a segment of one tile
-    x.ctas = min(max(x.total / (w.run_cost + 1), 1), w.ctas);
+    // small calls take as many CTAs as stretches of two places give
+    x.ctas = min(max(x.total / 2, 1), w.ctas);
     return x;
 }
 

@@ -50,7 +50,7 @@ using shared::Run;
 using shared::Work;
 
 constexpr int kBeforeWarps = 4;
-constexpr int kAfterWarps = 4;
+constexpr int kAfterWarps = 8;
 constexpr int kPrefixRows = 64;                // queries of a prefix segment on the CUDA cores
 constexpr int kOwnRows = 16;                   // rows of the tile that serves a sequence's own keys
 
@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(kBeforeWarps * 32) before_kernel(const BeforeP
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
     const int64_t rows = static_cast<int64_t>(p.w.batch) * p.w.heads * p.w.group;
+    let_following_start();
     if (blockIdx.x == 0) {                                    // places of the own keys, summed over the batch
         if (threadIdx.x >= 32) return;
         int before = 0;
@@ -184,6 +185,7 @@ __global__ void __launch_bounds__(kAfterWarps * 32) after_kernel(const AfterPara
     const int g = static_cast<int>(row % w.group);
     const int64_t sh = row / w.group;                         // sequence * heads + head
     const int h = static_cast<int>(sh % w.heads), b = static_cast<int>(sh / w.heads);
+    wait_for_previous();
     const Line x = shared::line_of(w, shared::own_start(w, w.batch));
 
     float m = -INFINITY, l = 0.0f, o[E];
@@ -338,6 +340,7 @@ __global__ void __launch_bounds__(core::kThreads) main_kernel(const MainParams p
     extern __shared__ float4 smem4[];
     __shared__ float cent[kMaxLevels];
     if (threadIdx.x < (1 << B)) cent[threadIdx.x] = p.cent[threadIdx.x];
+    wait_for_previous();
     const Line x = shared::line_of(p.w, shared::own_start(p.w, p.w.batch));
     if (blockIdx.x >= x.ctas) return;
     float *smem = reinterpret_cast<float *>(smem4);
@@ -380,8 +383,7 @@ cudaError_t launch_main(const SharedArgs &a, const Work &w, cudaStream_t stream)
                    p.sp_idx = dbg::span(a.idx, own * (D * B / 8));
                    p.sp_norms = dbg::span(a.norms, own * 4);
                    p.sp_V = dbg::span(a.V, own * D * sizeof(T));)
-    kernel<<<w.ctas, core::kThreads, kSmem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_following(kernel, p, dim3(w.ctas), core::kThreads, kSmem, stream);
 }
 
 template <int D, typename T>
@@ -447,12 +449,12 @@ cudaError_t launch_after_d(const SharedArgs &a, const Work &w, cudaStream_t stre
     const int rows = w.batch * w.heads * w.group;
     AXR_DEBUG_ONLY(p.sp_out = dbg::span(a.out, static_cast<uint64_t>(rows) * D * dtype_bytes(a.vdtype));
                    p.sp_lse = dbg::span(a.lse, a.lse ? 4ull * rows : 0);)
+    const unsigned threads = kAfterWarps * 32;
     switch (a.vdtype) {
-    case AXR_F32: after_kernel<D, float><<<rows, kAfterWarps * 32, 0, stream>>>(p); break;
-    case AXR_F16: after_kernel<D, __half><<<rows, kAfterWarps * 32, 0, stream>>>(p); break;
-    default: after_kernel<D, __nv_bfloat16><<<rows, kAfterWarps * 32, 0, stream>>>(p); break;
+    case AXR_F32: return launch_following(&after_kernel<D, float>, p, dim3(rows), threads, 0, stream);
+    case AXR_F16: return launch_following(&after_kernel<D, __half>, p, dim3(rows), threads, 0, stream);
+    default: return launch_following(&after_kernel<D, __nv_bfloat16>, p, dim3(rows), threads, 0, stream);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace

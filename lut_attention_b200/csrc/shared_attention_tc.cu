@@ -616,6 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         tmem_alloc(smem_u32(&B.tmem_base), 512);
         tmem_relinquish();
     }
+    wait_for_previous();
     if (p.w.batch <= kIndexed)
         for (int b = threadIdx.x; b <= p.w.batch; b += kThreads) {
             B.start[b] = shared::own_start(p.w, b);
@@ -664,8 +665,7 @@ cudaError_t launch(const Params &p, cudaStream_t stream)
     const auto kernel = shared_tc_kernel<D, B, kBF16>;
     cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), smem_bytes<D>(), done);
     if (e != cudaSuccess) return e;
-    kernel<<<p.w.ctas, kThreads, smem_bytes<D>(), stream>>>(p);
-    return cudaGetLastError();
+    return launch_following(kernel, p, dim3(p.w.ctas), kThreads, smem_bytes<D>(), stream);
 }
 
 template <int D, bool kBF16>
