@@ -624,7 +624,7 @@ bool make_map(CUtensorMap *map, const void *base, int dtype, int d, int rows, in
 {
     const EncodeTiledFn encode = encode_tiled();
     if (!encode) return false;
-    if (heads == 1) head = static_cast<int64_t>(rows) * row;   // unused
+    if (heads == 1) head = row;                                // unused, but it has limits too
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(heads)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row) * 2, static_cast<cuuint64_t>(head) * 2};
     const cuuint32_t b[3] = {64, static_cast<cuuint32_t>(box), 1}, es[3] = {1, 1, 1};
