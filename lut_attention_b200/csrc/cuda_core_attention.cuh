@@ -10,13 +10,19 @@
 // scores, keys tx + 16 j; of the output, D / 16 coordinates.  The 16 threads of
 // a query sit in one half-warp, so its statistics are shuffles and its weights
 // pass through shared memory behind a __syncwarp.  Rows are padded by 16 bytes,
-// which keeps the 16-byte reads of neighbouring rows free of bank conflicts.
+// which keeps the 16-byte reads of neighbouring rows free of bank conflicts.  Both
+// products are bound by the FMA pipes and run on pairs of fp32 numbers, which leaves
+// issue slots to the shared-memory reads: even and odd coordinates of a score in the
+// two halves, neighbouring coordinates of an output.
 #pragma once
 
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <type_traits>
+
+#include "packed_f32.cuh"
 
 namespace axr {
 namespace core {
@@ -59,7 +65,8 @@ struct Tile {
     using S = Shape<D>;
     static constexpr int R = BM / 16, C = S::BN / 16, E = S::E, W = S::W;
     float *q, *k, *v, *p;                        // q [BM][DS], k and v [BN][DS], p [BM][PS]
-    float m[R], l[R], o[R][E];
+    float m[R], l[R];
+    uint64_t o[R][E / 2];                        // pairs of coordinates
 
     __device__ explicit Tile(float *smem)
         : q(smem), k(q + BM * S::DS), v(k + S::BN * S::DS), p(v + S::BN * S::DS)
@@ -72,12 +79,19 @@ struct Tile {
             m[i] = -INFINITY;
             l[i] = 0.0f;
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[i][e] = 0.0f;
+            for (int e = 0; e < E / 2; ++e) o[i][e] = 0u;     // two zeros
         }
     }
     __device__ int ty() const { return threadIdx.x >> 4; }
     __device__ int tx() const { return threadIdx.x & 15; }
     __device__ int row(int i) const { return ty() + 16 * i; }
+    // output e of query row(i)
+    __device__ float out(int i, int e) const
+    {
+        float a, b;
+        packed::unpair(o[i][e / 2], a, b);
+        return e & 1 ? b : a;
+    }
     // output coordinate e of this thread
     __device__ int col(int e) const { return (e / W) * 16 * W + tx() * W + e % W; }
 
@@ -86,26 +100,33 @@ struct Tile {
     template <typename Limit>
     __device__ void step(Limit limit)
     {
+        using namespace packed;
         float s[R][C];
+        {
+            uint64_t s2[R][C];
 #pragma unroll
-        for (int i = 0; i < R; ++i)
+            for (int i = 0; i < R; ++i)
 #pragma unroll
-            for (int j = 0; j < C; ++j) s[i][j] = 0.0f;
+                for (int j = 0; j < C; ++j) s2[i][j] = 0u;    // two zeros
 #pragma unroll 2
-        for (int x = 0; x < D; x += 4) {
-            float4 a[R], b[C];
+            for (int x = 0; x < D; x += 4) {
+                ulonglong2 a[R], b[C];
 #pragma unroll
-            for (int i = 0; i < R; ++i) a[i] = *reinterpret_cast<const float4 *>(q + row(i) * S::DS + x);
+                for (int i = 0; i < R; ++i) a[i] = *reinterpret_cast<const ulonglong2 *>(q + row(i) * S::DS + x);
 #pragma unroll
-            for (int j = 0; j < C; ++j) b[j] = *reinterpret_cast<const float4 *>(k + (tx() + 16 * j) * S::DS + x);
+                for (int j = 0; j < C; ++j) b[j] = *reinterpret_cast<const ulonglong2 *>(k + (tx() + 16 * j) * S::DS + x);
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+#pragma unroll
+                    for (int j = 0; j < C; ++j) s2[i][j] = fma2(a[i].y, b[j].y, fma2(a[i].x, b[j].x, s2[i][j]));
+            }
 #pragma unroll
             for (int i = 0; i < R; ++i)
 #pragma unroll
                 for (int j = 0; j < C; ++j) {
-                    s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
-                    s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
-                    s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
-                    s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+                    float even, odd;
+                    unpair(s2[i][j], even, odd);
+                    s[i][j] = even + odd;
                 }
         }
 #pragma unroll
@@ -133,8 +154,9 @@ struct Tile {
             for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
             l[i] = fmaf(l[i], a, sum);
             m[i] = top;
+            const uint64_t a2 = pair(a, a);
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[i][e] *= a;
+            for (int e = 0; e < E / 2; ++e) o[i][e] = mul2(o[i][e], a2);
         }
         __syncwarp();
         for (int t = 0; t < S::BN; t += 4) {
@@ -143,23 +165,24 @@ struct Tile {
             for (int i = 0; i < R; ++i) w[i] = *reinterpret_cast<const float4 *>(p + row(i) * S::PS + t);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                float x[E];
+                uint64_t x[E / 2];
 #pragma unroll
                 for (int e = 0; e < E; e += W) {
                     const float *src = v + (t + u) * S::DS + col(e);
                     if constexpr (W == 4) {
-                        const float4 y = *reinterpret_cast<const float4 *>(src);
-                        x[e] = y.x; x[e + 1] = y.y; x[e + 2] = y.z; x[e + 3] = y.w;
+                        const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(src);
+                        x[e / 2] = y.x;
+                        x[e / 2 + 1] = y.y;
                     } else {
-                        const float2 y = *reinterpret_cast<const float2 *>(src);
-                        x[e] = y.x; x[e + 1] = y.y;
+                        x[e / 2] = *reinterpret_cast<const uint64_t *>(src);
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
                     const float wi = u == 0 ? w[i].x : u == 1 ? w[i].y : u == 2 ? w[i].z : w[i].w;
+                    const uint64_t w2 = pair(wi, wi);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) o[i][e] = fmaf(wi, x[e], o[i][e]);
+                    for (int e = 0; e < E / 2; ++e) o[i][e] = fma2(w2, x[e], o[i][e]);
                 }
             }
         }

@@ -44,9 +44,10 @@ __global__ void __launch_bounds__(core::kThreads) prompt_kernel(const Params p)
     using S = core::Shape<D>;
     extern __shared__ float4 smem4[];
     core::Tile<D, BM> t(reinterpret_cast<float *>(smem4));
-    const int hq = blockIdx.y, h = hq / p.s.group;
+    // the query heads of a tile are neighbours, so that the longest tiles of all go first
+    const int hqs = p.s.heads * p.s.group, hq = blockIdx.x % hqs, h = hq / p.s.group;
     PromptTile w;
-    if (!find_tile<BM>(p.s, blockIdx.x, w AXR_DEBUG_ONLY(, p.sp_cu_q, p.sp_cu_k))) return;
+    if (!find_tile<BM>(p.s, blockIdx.x / hqs, w AXR_DEBUG_ONLY(, p.sp_cu_q, p.sp_cu_k))) return;
 
     // rows of `rows` tokens from `row0` into padded shared rows, zeros past them
     auto fill = [&](float *dst, int count, const void *base, int64_t head, int64_t stride, int hh, int row0, int rows,
@@ -83,7 +84,7 @@ __global__ void __launch_bounds__(core::kThreads) prompt_kernel(const Params p)
 #pragma unroll
         for (int e = 0; e < t.E; ++e) {
             T *to = dst + t.col(e);
-            if (AXR_IN(p.sp_out, to, sizeof(T))) *to = core::from_f32<T>(t.o[i][e] * inv);
+            if (AXR_IN(p.sp_out, to, sizeof(T))) *to = core::from_f32<T>(t.out(i, e) * inv);
         }
         if (p.lse && t.tx() == 0) {
             float *to = p.lse + static_cast<int64_t>(hq) * p.s.total_q + at;
@@ -121,7 +122,9 @@ cudaError_t launch_dt(const PromptArgs &a, cudaStream_t stream)
                    p.sp_lse = dbg::span(a.lse, a.lse ? 4ull * hq * a.s.total_q : 0);
                    p.sp_cu_q = dbg::span(a.s.cu_q, 4ull * (a.s.batch + 1));
                    p.sp_cu_k = dbg::span(a.s.cu_k, 4ull * (a.s.batch + 1));)
-    kernel<<<dim3(prompt_tiles(a.s, BM), a.s.heads * a.s.group), core::kThreads, kSmem, stream>>>(p);
+    const int64_t grid = static_cast<int64_t>(prompt_tiles(a.s, BM)) * a.s.heads * a.s.group;
+    if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+    kernel<<<static_cast<unsigned>(grid), core::kThreads, kSmem, stream>>>(p);
     return cudaGetLastError();
 }
 

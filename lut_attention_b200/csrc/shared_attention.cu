@@ -326,7 +326,7 @@ __device__ void take_run(const MainParams &p, const Run &r, float *smem, const f
         float *dst = shared::slot(w, r, blockIdx.x, t.row(i));
         if (!AXR_IN((own ? w.sp_own_part : w.sp_prefix_part), dst, (D + 2) * 4)) continue;
 #pragma unroll
-        for (int e = 0; e < t.E; ++e) dst[t.col(e)] = t.o[i][e];
+        for (int e = 0; e < t.E; ++e) dst[t.col(e)] = t.out(i, e);
         if (t.tx() == 0) {
             dst[D] = t.m[i];
             dst[D + 1] = t.l[i];
