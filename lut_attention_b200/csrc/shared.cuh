@@ -49,9 +49,15 @@ struct Line {
     int own_first;                     // first place of the own segments
     int total;                         // below 2^31 (checked on the host)
     int ctas;                          // that take part
-    __device__ int begin(int c) const { return static_cast<int>(static_cast<int64_t>(total) * c / ctas); }
+    __device__ int begin(int c) const { return share(total, c, 0, ctas); }
     // the CTA that holds place t
-    __device__ int owner(int t) const { return static_cast<int>(((static_cast<int64_t>(t) + 1) * ctas - 1) / total); }
+    __device__ int owner(int t) const { return share(t + 1, ctas, 1, total); }
+    // (a * b - less) / c; in 32 bits, several times as fast, where all such products fit
+    __device__ int share(int a, int b, int less, int c) const
+    {
+        if (total <= INT32_MAX / ctas) return (a * b - less) / c;
+        return static_cast<int>((static_cast<int64_t>(a) * b - less) / c);
+    }
 };
 
 // places of a segment of `keys` keys

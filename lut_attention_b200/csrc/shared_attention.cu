@@ -50,7 +50,7 @@ using shared::Run;
 using shared::Work;
 
 constexpr int kBeforeWarps = 4;
-constexpr int kAfterWarps = 8;
+constexpr int kAfterWarps = 2;                 // of a query: more repeat the way to its slots, which costs more than their reading
 constexpr int kPrefixRows = 64;                // queries of a prefix segment on the CUDA cores
 constexpr int kOwnRows = 16;                   // rows of the tile that serves a sequence's own keys
 
@@ -182,43 +182,62 @@ __global__ void __launch_bounds__(kAfterWarps * 32) after_kernel(const AfterPara
     const Work &w = p.w;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t row = blockIdx.x;
-    const int g = static_cast<int>(row % w.group);
-    const int64_t sh = row / w.group;                         // sequence * heads + head
-    const int h = static_cast<int>(sh % w.heads), b = static_cast<int>(sh / w.heads);
+    const int sh = blockIdx.x / w.group, g = blockIdx.x - sh * w.group;     // sequence * heads + head, query of the group
+    const int b = sh / w.heads, h = sh - b * w.heads;
     wait_for_previous();
     const Line x = shared::line_of(w, shared::own_start(w, w.batch));
 
     float m = -INFINITY, l = 0.0f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.0f;
-    // one slot's (o, m, l) into this warp's sums
-    auto add = [&](const float *src AXR_DEBUG_ONLY(, const dbg::Span &sp)) {
-        if (!AXR_IN(sp, src, (D + 2) * 4)) return;
-        const float sm = src[D], sl = src[D + 1];
-        float v[E];
+    // slots c0 + warp, c0 + warp + kAfterWarps, ... to c1 into this warp's sums; `at(c)`
+    // is slot c.  kAhead of them are read before the first is used.
+    auto add = [&](int c0, int c1, auto at AXR_DEBUG_ONLY(, const dbg::Span &sp)) {
+        constexpr int kAhead = 4;
+        for (int c = c0 + warp; c <= c1; c += kAhead * kAfterWarps) {
+            float sm[kAhead], sl[kAhead], v[kAhead][E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = src[e * 32 + lane];
-        const float top = fmaxf(m, sm);
-        const float base = top == -INFINITY ? 0.0f : top;
-        const float a = exp2f(m - base), c = exp2f(sm - base);
-        l = fmaf(l, a, sl * c);
+            for (int y = 0; y < kAhead; ++y) {
+                const float *src = at(c + y * kAfterWarps);
+                const bool there = c + y * kAfterWarps <= c1 && AXR_IN(sp, src, (D + 2) * 4);
+                sm[y] = there ? src[D] : -INFINITY;
+                sl[y] = there ? src[D + 1] : 0.0f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], a, v[e] * c);
-        m = top;
+                for (int e = 0; e < E; ++e) v[y][e] = there ? src[e * 32 + lane] : 0.0f;
+            }
+            float top = m;
+#pragma unroll
+            for (int y = 0; y < kAhead; ++y) top = fmaxf(top, sm[y]);
+            const float base = top == -INFINITY ? 0.0f : top;
+            const float f = exp2f(m - base);
+            m = top;
+            l *= f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll
+            for (int y = 0; y < kAhead; ++y) {
+                const float z = exp2f(sm[y] - base);
+                l = fmaf(sl[y], z, l);
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = fmaf(v[y][e], z, o[e]);
+            }
+        }
     };
     if (x.prefix_places > 0) {
         const int at = b * w.group + g;
         const int seg = h * w.row_tiles + at / w.bm;
         const int c0 = x.owner(seg * x.prefix_places + w.run_cost), c1 = x.owner((seg + 1) * x.prefix_places - 1);
-        for (int c = c0 + warp; c <= c1; c += kAfterWarps)
-            add(w.prefix_part + (static_cast<int64_t>(seg + c) * w.slot_rows + at % w.bm) * (D + 2) AXR_DEBUG_ONLY(, w.sp_prefix_part));
+        const float *slots = w.prefix_part + (static_cast<int64_t>(seg) * w.slot_rows + at % w.bm) * (D + 2);
+        const int step = w.slot_rows * (D + 2);
+        add(c0, c1, [&](int c) { return slots + static_cast<int64_t>(c) * step; } AXR_DEBUG_ONLY(, w.sp_prefix_part));
     }
     const int s0 = shared::own_start(w, b), per = shared::own_start(w, b + 1) - s0;
     if (per > 0) {
         const int t0 = x.own_first + w.heads * s0 + h * per;
         const int c0 = x.owner(t0 + w.run_cost), c1 = x.owner(t0 + per - 1);
-        for (int c = c0 + warp; c <= c1; c += kAfterWarps)
-            add(w.own_part + ((sh + c) * w.group + g) * (D + 2) AXR_DEBUG_ONLY(, w.sp_own_part));
+        const float *slots = w.own_part + (static_cast<int64_t>(sh) * w.group + g) * (D + 2);
+        const int step = w.group * (D + 2);
+        add(c0, c1, [&](int c) { return slots + static_cast<int64_t>(c) * step; } AXR_DEBUG_ONLY(, w.sp_own_part));
     }
     if (lane == 0) {
         s_m[warp] = m;
