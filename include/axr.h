@@ -287,13 +287,14 @@ int axr_select_signs(const void *K, int kdtype, const void *q, int qdtype, int64
  * strides  HOST int64[8], read before the call returns: elements between heads
  *          and between rows of q, of K, of V and of out, in this order.  Rows
  *          are contiguous; all strides are >= 0 and multiples of 16 bytes.  Row
- *          strides are >= d.
+ *          strides are >= d.  Rows of out must not overlap: head by head, or row by
+ *          row with the heads inside (q, K and V may be broadcast over heads).
  * out      device, heads*group x total_q rows of d elements of dtype; must not
  *          overlap the inputs.
  * lse      device float[(heads*group) * total_q], or NULL.
  * q, K, V, out 16-byte aligned.  d a power of two in [32, 512]; group in [1, 8];
- * total_q, total_k at most 2^31 - 1; at most 65535 query heads.  total_q == 0 or batch == 0 is a
- * no-op.  The products are exact or accumulated in fp32, the softmax is fp32;
+ * total_q, total_k at most 2^31 - 1; at most 65535 query heads, and 2^31 - 1 tiles of 32 queries
+ * (total_q / 32 + batch, each query head for itself).  total_q == 0 or batch == 0 is a no-op.  The products are exact or accumulated in fp32, the softmax is fp32;
  * for 16-bit types with d = 64, 128 and 256 the weights p are rounded to dtype
  * for the product with V.  One kernel on `stream`, no workspace.
  */

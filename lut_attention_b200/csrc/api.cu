@@ -1,5 +1,6 @@
 // extern "C" entry points of libaxr: argument validation, codebook lookup and
 // kernel launch.  Every check runs on the host before anything is enqueued.
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -496,6 +497,9 @@ extern "C" int axr_prompt_attention(const void *q, const void *K, const void *V,
         return fail(AXR_EUNSUPPORTED, "at most 2^31-1 packed rows");
     if ((int64_t)heads * group > 65535) return fail(AXR_EUNSUPPORTED, "%d x %d query heads: at most 65535", heads, group);
     if (total_q == 0 || batch == 0) return ok();
+    if (std::min(total_q / 32 + batch, total_q) * heads * group > (int64_t)INT32_MAX)   // a grid of the smallest tiles
+        return fail(AXR_EUNSUPPORTED, "%lld rows of %d sequences: at most 2^31-1 tiles of 32 queries over all heads",
+                    (long long)total_q, batch);
     if (!strides) return fail(AXR_EINVAL, "strides is NULL");
     static const char *const names[4] = {"q", "K", "V", "out"};
     for (int i = 0; i < 4; ++i) {
@@ -504,6 +508,11 @@ extern "C" int axr_prompt_attention(const void *q, const void *K, const void *V,
             return fail(AXR_EINVAL, "strides of %s (%lld, %lld): multiples of 16 bytes, rows at least d apart", names[i],
                         (long long)hd, (long long)row);
     }
+    const int64_t hq = (int64_t)heads * group, o_head = strides[6], o_row = strides[7];
+    // rows of out lie head by head, or row by row with the heads inside (products may pass 64 bits)
+    if (hq > 1 && (__int128)(total_q - 1) * o_row + d > o_head &&
+        (o_head < d || (__int128)(hq - 1) * o_head + d > o_row))
+        return fail(AXR_EINVAL, "strides of out (%lld, %lld): rows overlap", (long long)o_head, (long long)o_row);
     if ((rc = check_device_ptr(q, 16, "q")) != AXR_OK) return rc;
     if (total_k > 0) {
         if ((rc = check_device_ptr(K, 16, "K")) != AXR_OK) return rc;

@@ -36,8 +36,8 @@ struct PromptTile {
 // tiles of `bm` queries that `batch` sequences of `total_q` queries can have at most
 inline int prompt_tiles(const PromptShape &s, int bm)
 {
-    const int64_t full = s.total_q / bm, ragged = s.batch < s.total_q ? s.batch : s.total_q;
-    return static_cast<int>(full + ragged);
+    const int64_t most = s.total_q / bm + static_cast<int64_t>(s.batch);
+    return static_cast<int>(most < s.total_q ? most : s.total_q);
 }
 
 // The tile of BM queries that comes `index`-th over all sequences; false past the

@@ -46,6 +46,37 @@ def test_prompt_refusals(axr_lib):
     del keep
 
 
+def test_prompt_refuses_overlapping_rows_of_out(axr_lib):
+    """out by heads, or by rows with the heads inside; anything else would be written twice."""
+    f = axr_lib.axr_prompt_attention
+    keep, p = _buf()
+
+    def call(o_head, o_row, tq=10, heads=2, group=2):
+        st = (ctypes.c_int64 * 8)(1280, 128, 1280, 128, 1280, 128, o_head, o_row)
+        rc = f(p, p, p, 2, tq, 10, p, p, 1, heads, group, 128, ctypes.addressof(st), p, p, None)
+        return rc, axr_lib.axr_last_error()
+
+    for bad in ((0, 128), (128, 128), (128, 384), (1272, 128), (64, 512), (1 << 62, 1 << 62)):
+        rc, why = call(*bad)
+        assert rc == INV and b"overlap" in why, bad
+    for good in ((1280, 128), (128, 512), (136, 3 * 136 + 128), (9 * 200 + 128, 200)):
+        rc, why = call(*good)
+        assert rc == INV and b"device" in why, good            # as far as the host memory
+    assert b"device" in call(0, 128, heads=1, group=1)[1] and b"device" in call(128, 128, tq=1)[1]
+    del keep
+
+
+def test_prompt_refuses_more_tiles_than_a_grid(axr_lib):
+    f = axr_lib.axr_prompt_attention
+    keep, p = _buf()
+    st = (ctypes.c_int64 * 8)(*([128, 128] * 4))
+    call = lambda tq, batch, heads: f(p, p, p, 2, tq, 10, p, p, batch, heads, 1, 128, ctypes.addressof(st), p, p, None)
+    most = (1 << 31) - 1
+    assert call(most, most, 2) == UNS and call(most, 1, 33) == UNS and call(1 << 20, 1 << 20, 2048) == UNS
+    assert call(most, most, 1) == INV and b"device" in axr_lib.axr_last_error()
+    del keep
+
+
 def test_shared_refusals(axr_lib):
     f, ws = axr_lib.axr_attention_shared, axr_lib.axr_attention_shared_workspace_bytes
     keep, p = _buf()

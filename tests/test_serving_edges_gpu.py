@@ -139,6 +139,53 @@ def test_shared_zero_and_extreme_queries_and_norms():
     _check_shared(q, pre, own, [50, 0, 17], 2, b, _signs(d), out, lse)
 
 
+def test_shared_weights_and_evict_past_32_bit_offsets():
+    """A head of 2^24 + 5 rows: its values pass 2^32 bytes and 2^31 elements.  All norms
+    but those of the last rows are 0, so the other keys score 0 with values of 0."""
+    n, tail, group, d, b = (1 << 24) + 5, 300, 4, 128, 4
+    idx = torch.zeros((1, n, d * b // 8), dtype=torch.uint8, device=DEV)
+    norms = torch.zeros((1, n), device=DEV)
+    V = torch.zeros((1, n, d), dtype=BF16, device=DEV)
+    last = _cache(1, tail, d, b, BF16, seed=9)
+    for whole, part in zip((idx, norms, V), last):
+        whole[:, n - tail:] = part
+    norms[:, n - tail:] += 30.0
+    small = [t[:, n - tail:] for t in (idx, norms, V)]
+    q, signs = _randn((group, d), 10, BF16), _signs(d)
+    empty = [t[:, :0].contiguous() for t in small]
+
+    # a: the long head as the prefix; b: as a sequence's own cache
+    cent = torch.from_numpy(axr.axr_make_codebook(d, b)[0]).to(DEV)
+    want, lse_t, tol, tol_lse = plain.shared(q, [t.contiguous() for t in small], empty, [0], group, b, signs, cent, 2.0 ** -8,
+                                       3 * 2.0 ** -22)
+    lse = torch.logaddexp(lse_t, torch.full_like(lse_t, math.log(n - tail)))     # n - tail keys of score 0
+    shrink = torch.exp(lse_t - lse)[:, None]
+    A = last[2].double().abs().amax(1)                                           # |V| bound of the weighted sums
+    # a CTA of at least 100 adds up at most n / 100 weights, rounding 2^-24 each, and 1000 more in the merge
+    sums = (n / 100 + 1000) * 2.0 ** -24
+    for pre, own, length in (((idx, norms, V), empty, 0), (empty, (idx, norms, V), n)):
+        out, got = axr.axr_attention_shared(q, *pre, *own, _int32([length]), group, b, signs)
+        _within(out, want * shrink, (tol + 2 * sums * A) * shrink, "out")
+        _within(got, lse, tol_lse + sums + 2.0 ** -20, "lse")
+
+    # the weights of a step that looks at the head's ends, then the choice by them
+    scores = torch.full((group, n), -30.0, device=DEV)
+    scores[:, :50] = 3.0
+    scores[:, n - tail:n - 200] = 2.0
+    w = torch.zeros((1, n), device=DEV)
+    axr.axr_accumulate_weights(scores, w, group)
+    total = 50 * math.exp(3.0) + 100 * math.exp(2.0) + (n - 150) * math.exp(-30.0)
+    # a thread adds up n / 4096 weights, exponents up to 33 round by 33 2^-23: below 2^-11
+    for part, x in ((w[0, :50], 3.0), (w[0, n - tail:n - 200], 2.0)):
+        assert ((part.double() * total / (group * math.exp(x)) - 1).abs() <= 2.0 ** -11).all()
+    got = axr.axr_evict(idx, norms, V, w, _int32([n]), 250, 100)
+    rows = list(range(50)) + list(range(n - tail, n - 200)) + list(range(n - 100, n))
+    assert got[4][0].tolist() == rows
+    at = torch.tensor(rows, device=DEV)
+    assert torch.equal(got[0][0], idx[0, at]) and torch.equal(got[1][0], norms[0, at]) and torch.equal(got[2][0], V[0, at])
+    assert axr.axr_device_status() == 0
+
+
 @pytest.mark.parametrize("n,keep", [(8191, 100), (8193, 4000), (250001, 1000), (250001, 200000)])
 def test_evict_long_caches(n, keep):
     cache = _cache(1, n, 32, 1, F16, seed=4)

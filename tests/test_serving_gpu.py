@@ -178,8 +178,9 @@ def _signs(d):
 
 
 def _u_cent(vdtype, d):
-    """Centroids are held in fp16 (scaled to round by at most 2^-13) where the tensor cores take them."""
-    return 0.0 if vdtype == F32 else 2.0 ** -13
+    """For 16-bit values queries and centroids are pairs of fp16 parts: 2^-22 each, and
+    the product of the two low parts, left out, another 2^-22."""
+    return 0.0 if vdtype == F32 else 3 * 2.0 ** -22
 
 
 def _check_shared(q, pre, own, lengths, group, b, signs, out, lse):
