@@ -8,7 +8,9 @@
 // CTA: one pass for the running (m, l) of every query, an exchange of the
 // kCluster partial (m, l) through distributed shared memory, and a second pass
 // that adds the weights (its scores come from L2).  4 G bytes per key are read
-// twice and 8 bytes of w moved once.
+// twice and 8 bytes of w moved once.  32 heads of 131072 keys, G = 4: 41 us, 2.4 TB/s of
+// those 100 MB with the second reading from L2; bound by its instructions (issue 42 %, the
+// special function unit 40 % busy) and the two passes' latencies.  4-byte loads: 51 us.
 //
 // Eviction of head h with len rows, of which the last `recent` stay anyway:
 // among t < len - recent the k = keep - recent rows of largest weight stay,
@@ -17,10 +19,12 @@
 // holds the sign, the exponent and 2 bits: 8 would put nearly all weights into two or
 // three counters): the head's cluster counts its keys per digit in shared memory, each
 // CTA adds up an eighth of the counters over the cluster for all of it (distributed
-// shared memory; adding to one CTA's counters took four times as long), and the digit
+// shared memory; with all counts added to one CTA's the choice took 58 us), and the digit
 // that holds rank k is fixed.  Then one ordered pass writes the slots that stay (all
 // above the k-th key, and the first of those equal to it), and a second kernel copies
-// the rows: it starts while the choice ends and is bound by the rows' bytes.
+// the rows: it starts while the choice ends and is bound by the rows' bytes.  32 heads,
+// 32768 rows to 8192 (d = 128, b = 4, bf16): 25 us for the choice, bound by its barriers, and
+// 33 us for the copy, 5.2 TB/s in and out.
 #include <cooperative_groups.h>
 
 #include "axr_internal.cuh"

