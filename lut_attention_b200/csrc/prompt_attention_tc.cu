@@ -12,7 +12,9 @@
 // makes the rescale rare enough for the softmax warps to do it themselves.
 //
 // A persistent CTA per SM with one TMA warp, one MMA warp and a softmax
-//   d <= 128: two query tiles (256 queries).  Their S take turns: while the tensor
+//   d <= 128: two query tiles, of two heads of a group or, in an odd group, of 256
+//     queries.  (Two heads see the same keys, and leave fewer rows of a ragged sequence's
+//     last tile empty: 12 prompts of 1 to 1365 tokens 192 us, by 256 queries 209.) Their S take turns: while the tensor
 //     cores run one tile's products, the other tile's warps are in their softmax.
 //   d = 256: one query tile (O takes half of tensor memory) with two S buffers;
 //     the products of the next tile of keys run under the softmax of this one.
@@ -93,14 +95,14 @@ struct Params {
     void *out;
     float *lse;
     float scale;               // log2(e) / sqrt(d)
-    int tiles;                 // items per query head (at most)
+    int64_t items;             // at most
     AXR_DEBUG_ONLY(dbg::Span sp_out, sp_lse, sp_cu_q, sp_cu_k;)
 };
 
 // What an item's roles need to know.
 struct Item {
     PromptTile t;
-    int hq;
+    int hq;                    // of query tile 0
     int rows[2];               // queries of each query tile
     int n[2];                  // tiles of keys each of them sees
     int most;                  // tiles of keys loaded
@@ -113,17 +115,25 @@ __device__ __forceinline__ int64_t item_of(int turn)
     return static_cast<int64_t>(turn) * gridDim.x + at;
 }
 
-template <int D>
+// kPair: the two query tiles are the same rows of neighbouring heads of a group, else
+// neighbouring rows of one head
+template <bool kPair>
+__device__ __forceinline__ int first_row(const Item &x, int t) { return x.t.row + (kPair ? 0 : t * kTile); }
+template <bool kPair>
+__device__ __forceinline__ int head(const Item &x, int t) { return x.hq + (kPair ? t : 0); }
+
+template <int D, bool kPair>
 __device__ __forceinline__ bool item_at(const Params &p, int64_t i, Item &x)
 {
     using C = Cfg<D>;
-    const int hqs = p.s.heads * p.s.group;
-    x.hq = static_cast<int>(i % hqs);
-    if (!find_tile<C::BM>(p.s, static_cast<int>(i / hqs), x.t AXR_DEBUG_ONLY(, p.sp_cu_q, p.sp_cu_k))) return false;
+    static_assert(!kPair || C::NQ == 2, "two query tiles");
+    const int heads = p.s.heads * p.s.group / (kPair ? 2 : 1);
+    x.hq = static_cast<int>(i % heads) * (kPair ? 2 : 1);
+    if (!find_tile<kPair ? kTile : C::BM>(p.s, static_cast<int>(i / heads), x.t AXR_DEBUG_ONLY(, p.sp_cu_q, p.sp_cu_k))) return false;
     x.most = 0;
 #pragma unroll
     for (int t = 0; t < C::NQ; ++t) {
-        const int first = x.t.row + t * kTile;
+        const int first = first_row<kPair>(x, t);
         x.rows[t] = min(max(x.t.len_q - first, 0), kTile);
         const int keys = x.rows[t] > 0 ? max(first + x.rows[t] + x.t.len_k - x.t.len_q, 0) : 0;
         x.n[t] = (keys + kTile - 1) / kTile;
@@ -134,7 +144,7 @@ __device__ __forceinline__ bool item_at(const Params &p, int64_t i, Item &x)
 
 // Softmax of half `half` of every tile of keys for query tile t (buffer t; at
 // NQ = 1 buffers 0 and 1 in turn).  Thread = query.
-template <int D, bool kBF16>
+template <int D, bool kPair, bool kBF16>
 __device__ void softmax_role(const Params &p, Book &B, int t, int half, uint32_t tmem)
 {
     using C = Cfg<D>;
@@ -142,7 +152,6 @@ __device__ void softmax_role(const Params &p, Book &B, int t, int half, uint32_t
     const int r = warp * 32 + lane;                            // query of the tile
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t o_at = tmem + lanes + C::OCol + t * D + half * (D / 2);   // this half's columns of O
-    const int64_t items = static_cast<int64_t>(p.tiles) * p.s.heads * p.s.group;
     const int meet_id = 1 + t * 4 + warp;
     // a wait that runs out records a bit; the role then goes on without waiting, to
     // keep meeting its partner
@@ -156,12 +165,12 @@ __device__ void softmax_role(const Params &p, Book &B, int t, int half, uint32_t
     uint32_t count = 0;                                        // tiles so far: phases of s_full and o_done
     for (int turn = 0;; ++turn) {
         const int64_t i = item_of(turn);
-        if (i >= items) break;
+        if (i >= p.items) break;
         Item x;
-        if (!item_at<D>(p, i, x)) break;
+        if (!item_at<D, kPair>(p, i, x)) break;
         const int rows = t == 0 ? x.rows[0] : x.rows[1], n = t == 0 ? x.n[0] : x.n[1];
         const bool idle = warp * 32 >= rows;                   // no query of these warps
-        const int first = x.t.row + t * kTile + warp * 32;     // the warps' first query
+        const int first = first_row<kPair>(x, t) + warp * 32;     // the warps' first query
         const int past = x.t.len_k - x.t.len_q;
         float m = -INFINITY, l = 0.0f;
         for (int j = 0; j < n; ++j, ++count) {
@@ -246,9 +255,10 @@ __device__ void softmax_role(const Params &p, Book &B, int t, int half, uint32_t
             meet_partner(meet_id);
         }
         if (m == -INFINITY && l == l) l = 0.0f;                // no key: masked weights are 2^-126, not 0
-        const int64_t at = x.t.first_q + x.t.row + t * kTile + r;
+        const int64_t at = x.t.first_q + first_row<kPair>(x, t) + r;
+        const int hq = head<kPair>(x, t);
         const float inv = l > 0.0f ? 1.0f / l : l;             // 0 for no key, NaN stays NaN
-        char *dst = static_cast<char *>(p.out) + (x.hq * p.s.o_head + at * p.s.o_row + half * (D / 2)) * 2;
+        char *dst = static_cast<char *>(p.out) + (hq * p.s.o_head + at * p.s.o_row + half * (D / 2)) * 2;
 #pragma unroll 1
         for (int c = 0; c < D / 2; c += 32) {
             uint32_t o[32];
@@ -272,7 +282,7 @@ __device__ void softmax_role(const Params &p, Book &B, int t, int half, uint32_t
             }
         }
         if (p.lse && half == 0 && r < rows) {
-            float *to = p.lse + static_cast<int64_t>(x.hq) * p.s.total_q + at;
+            float *to = p.lse + static_cast<int64_t>(hq) * p.s.total_q + at;
             const float base = m == -INFINITY ? -INFINITY : m * p.scale - kBias<kBF16>;
             if (AXR_IN(p.sp_lse, to, 4)) *to = (base + log2f(l)) * kLn2;
         }
@@ -280,12 +290,11 @@ __device__ void softmax_role(const Params &p, Book &B, int t, int half, uint32_t
     }
 }
 
-template <int D>
+template <int D, bool kPair>
 __device__ void tma_role(const Params &p, Book &B, uint8_t *ring_ptr, uint32_t q_smem, uint32_t ring)
 {
     using C = Cfg<D>;
     const int lane = threadIdx.x & 31;
-    const int64_t items = static_cast<int64_t>(p.tiles) * p.s.heads * p.s.group;
     uint32_t pieces = 0, tails = 0, q_count[2] = {0, 0};
     bool ok = true;
     // the next stage of the ring, once it is free
@@ -300,9 +309,9 @@ __device__ void tma_role(const Params &p, Book &B, uint8_t *ring_ptr, uint32_t q
     };
     for (int turn = 0;; ++turn) {
         const int64_t i = item_of(turn);
-        if (i >= items) break;
+        if (i >= p.items) break;
         Item x;
-        if (!item_at<D>(p, i, x)) break;
+        if (!item_at<D, kPair>(p, i, x)) break;
         if (lane == 0 && ok) {
             const int h = x.hq / p.s.group;
             auto load_q = [&](int t) {
@@ -316,7 +325,7 @@ __device__ void tma_role(const Params &p, Book &B, uint8_t *ring_ptr, uint32_t q
                 mbar_arrive_expect_tx(bar, C::QBytes);
                 for (int c = 0; c < C::QBlocks; ++c)
                     tma_load_3d(q_smem + t * C::QBytes + c * kTile * 128, &p.q, c * 64,
-                                x.t.first_q + x.t.row + t * kTile, x.hq, bar);
+                                x.t.first_q + first_row<kPair>(x, t), head<kPair>(x, t), bar);
                 return true;
             };
             auto load_k = [&](int j) {
@@ -550,17 +559,16 @@ struct Products {
     }
 };
 
-template <int D, bool kBF16>
+template <int D, bool kPair, bool kBF16>
 __device__ void mma_role(const Params &p, Book &B, uint32_t q_smem, uint32_t ring, uint32_t tmem)
 {
     using C = Cfg<D>;
-    const int64_t items = static_cast<int64_t>(p.tiles) * p.s.heads * p.s.group;
     Products<D, kBF16> x(B, q_smem, ring, tmem);
     for (int turn = 0;; ++turn) {
         const int64_t i = item_of(turn);
-        if (i >= items) break;
+        if (i >= p.items) break;
         Item it;
-        if (!item_at<D>(p, i, it)) break;
+        if (!item_at<D, kPair>(p, i, it)) break;
         bool ok = true;
         if (elect_one()) ok = C::NQ == 2 ? x.item2(it.n[0], it.n[1], it.most) : x.item1(it.most);
         if (__any_sync(0xffffffffu, !ok)) break;
@@ -571,7 +579,7 @@ __device__ void mma_role(const Params &p, Book &B, uint32_t q_smem, uint32_t rin
     mbar_wait_warp(smem_u32(&B.drain), 0);
 }
 
-template <int D, bool kBF16>
+template <int D, bool kPair, bool kBF16>
 __global__ void __launch_bounds__(Cfg<D>::Threads, 1) prompt_tc_kernel(const __grid_constant__ Params p)
 {
     using C = Cfg<D>;
@@ -612,10 +620,10 @@ __global__ void __launch_bounds__(Cfg<D>::Threads, 1) prompt_tc_kernel(const __g
     tc_fence_after_sync();
     const uint32_t tmem = B.tmem_base;
     if (warp < C::SoftmaxWarps) {
-        softmax_role<D, kBF16>(p, B, warp >> 3, (warp >> 2) & 1, tmem);
+        softmax_role<D, kPair, kBF16>(p, B, warp >> 3, (warp >> 2) & 1, tmem);
     } else {
-        if (warp == C::WarpTma) tma_role<D>(p, B, ring_ptr, q_smem, ring);
-        else if (warp == C::WarpMma) mma_role<D, kBF16>(p, B, q_smem, ring, tmem);
+        if (warp == C::WarpTma) tma_role<D, kPair>(p, B, ring_ptr, q_smem, ring);
+        else if (warp == C::WarpMma) mma_role<D, kPair, kBF16>(p, B, q_smem, ring, tmem);
     }
     __syncwarp();
     tc_fence_before_sync();
@@ -640,20 +648,28 @@ bool make_map(CUtensorMap *map, const void *base, int dtype, int d, int rows, in
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool kBF16>
-cudaError_t launch(Params &p, const PromptArgs &a, cudaStream_t stream)
+template <int D, bool kPair, bool kBF16>
+cudaError_t launch_as(Params &p, const PromptArgs &a, cudaStream_t stream)
 {
     using C = Cfg<D>;
     static std::atomic<unsigned long long> done{0};
-    const auto kernel = prompt_tc_kernel<D, kBF16>;
+    const auto kernel = prompt_tc_kernel<D, kPair, kBF16>;
     cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void *>(kernel), smem_bytes<D>(), done);
     if (e != cudaSuccess) return e;
-    p.tiles = prompt_tiles(a.s, C::BM);
+    p.items = static_cast<int64_t>(prompt_tiles(a.s, kPair ? kTile : C::BM)) * (a.s.heads * a.s.group / (kPair ? 2 : 1));
     p.scale = kLog2e / sqrtf(static_cast<float>(D));
-    const int64_t items = static_cast<int64_t>(p.tiles) * a.s.heads * a.s.group;
     const int sms = device_sm_count();
-    kernel<<<items < sms ? static_cast<int>(items) : sms, C::Threads, smem_bytes<D>(), stream>>>(p);
+    kernel<<<p.items < sms ? static_cast<int>(p.items) : sms, C::Threads, smem_bytes<D>(), stream>>>(p);
     return cudaGetLastError();
+}
+
+template <int D, bool kBF16>
+cudaError_t launch(Params &p, const PromptArgs &a, cudaStream_t stream)
+{
+    if constexpr (Cfg<D>::NQ == 2) {
+        if (a.s.group % 2 == 0) return launch_as<D, true, kBF16>(p, a, stream);
+    }
+    return launch_as<D, false, kBF16>(p, a, stream);
 }
 
 bool make_params(const PromptArgs &a, Params &p)
