@@ -426,9 +426,11 @@ def _require_rows(t: torch.Tensor, name: str) -> None:
 def _row_strides(t: torch.Tensor) -> tuple[int, int]:
     """Element strides of heads and rows; those of an axis of length 1 are free and
     are given as a dense tensor has them."""
-    rows, d = t.shape[1], t.shape[2]
-    row = t.stride(1) if rows > 1 else d
-    return (t.stride(0) if t.shape[0] > 1 else rows * row), row
+    heads, rows, d = t.shape
+    head, row, _ = t.stride()
+    if rows <= 1:
+        row = d
+    return (head if heads > 1 else rows * row), row
 
 
 def _check_int32(t: torch.Tensor, name: str, count: int) -> None:
@@ -452,7 +454,7 @@ def axr_prompt_attention(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q
             raise ValueError("q, K and V must share a dtype: float32, float16 or bfloat16")
     hq, total_q, d = q.shape
     heads, total_k = K.shape[:2]
-    if tuple(V.shape) != tuple(K.shape) or K.shape[2] != d:
+    if V.shape != K.shape or K.shape[2] != d:
         raise ValueError(f"K and V must both be (heads, total_k, {d})")
     if heads < 1 or hq % heads:
         raise ValueError("q must have heads*group heads")
@@ -467,9 +469,10 @@ def axr_prompt_attention(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q
         out = torch.empty_like(q)
     if lse is None:
         lse = torch.empty((hq, total_q), dtype=torch.float32, device=q.device)
+    else:
+        _require_cuda(lse, "lse")
     _require_rows(out, "out")
-    _require_cuda(lse, "lse")
-    if out.dtype != q.dtype or tuple(out.shape) != tuple(q.shape) or lse.dtype != torch.float32 \
+    if out.dtype != q.dtype or out.shape != q.shape or lse.dtype != torch.float32 \
             or lse.numel() < hq * total_q:
         raise ValueError("out must be like q and lse float32 with heads*group*total_q elements")
     strides = (ctypes.c_int64 * 8)(*_row_strides(q), *_row_strides(K), *_row_strides(V), *_row_strides(out))
@@ -520,14 +523,17 @@ def axr_attention_shared(q: torch.Tensor, prefix_idx: torch.Tensor, prefix_norms
     if group < 1 or rows % (heads * group):
         raise ValueError("q must have batch*heads*group rows")
     batch = rows // (heads * group)
-    if tuple(prefix_norms.shape) != (heads, n) or tuple(prefix_V.shape) != (heads, n, d):
+    if prefix_norms.shape != (heads, n) or prefix_V.shape != (heads, n, d):
         raise ValueError(f"prefix_norms must be ({heads}, {n}) and prefix_V ({heads}, {n}, {d})")
     if idx.dim() != 3 or idx.shape[0] != batch * heads or idx.shape[2] != P:
         raise ValueError(f"idx must be (batch*heads={batch * heads}, capacity, {P})")
     capacity = idx.shape[1]
-    if tuple(norms.shape) != (batch * heads, capacity) or tuple(V.shape) != (batch * heads, capacity, d):
+    if norms.shape != (batch * heads, capacity) or V.shape != (batch * heads, capacity, d):
         raise ValueError(f"norms must be ({batch * heads}, {capacity}) and V ({batch * heads}, {capacity}, {d})")
     _check_int32(lengths, "lengths", batch)
+    for t, name in ((out, "out"), (lse, "lse"), (workspace, "workspace")):
+        if t is not None:
+            _require_cuda(t, name)
     if out is None:
         out = torch.empty((rows, d), dtype=V.dtype, device=q.device)
     if lse is None:
@@ -535,8 +541,6 @@ def axr_attention_shared(q: torch.Tensor, prefix_idx: torch.Tensor, prefix_norms
     if workspace is None:
         need = _shared_workspace_bytes(batch, heads, group, d, q.device)
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-    for t, name in ((out, "out"), (lse, "lse"), (workspace, "workspace")):
-        _require_cuda(t, name)
     if out.dtype != V.dtype or out.numel() < rows * d or lse.dtype != torch.float32 or lse.numel() < rows:
         raise ValueError("out must be of V's dtype and lse float32, both large enough")
     _call("axr_attention_shared", q.device, stream,
@@ -588,8 +592,8 @@ def axr_evict(idx: torch.Tensor, norms: torch.Tensor, V: torch.Tensor, weights: 
     heads, capacity, d = V.shape
     P = idx.shape[2]
     b = P * 8 // d if d else 0
-    if tuple(idx.shape) != (heads, capacity, packed_row_bytes(d, b)) or tuple(norms.shape) != (heads, capacity) \
-            or tuple(weights.shape) != (heads, capacity):
+    if idx.shape != (heads, capacity, packed_row_bytes(d, b)) or norms.shape != (heads, capacity) \
+            or weights.shape != (heads, capacity):
         raise ValueError(f"idx must be ({heads}, {capacity}, d*b/8), norms and weights ({heads}, {capacity})")
     _check_int32(lengths, "lengths", heads)
     if not 0 <= recent <= keep or keep < 1:
@@ -610,8 +614,8 @@ def axr_evict(idx: torch.Tensor, norms: torch.Tensor, V: torch.Tensor, weights: 
     _check_read_operands(idx_o, norms_o)
     capacity_o = V_o.shape[1] if V_o.dim() == 3 else -1
     if V_o.dtype != V.dtype or weights_o.dtype != torch.float32 or capacity_o < keep \
-            or tuple(V_o.shape) != (heads, capacity_o, d) or tuple(idx_o.shape) != (heads, capacity_o, P) \
-            or tuple(norms_o.shape) != (heads, capacity_o) or tuple(weights_o.shape) != (heads, capacity_o):
+            or V_o.shape != (heads, capacity_o, d) or idx_o.shape != (heads, capacity_o, P) \
+            or norms_o.shape != (heads, capacity_o) or weights_o.shape != (heads, capacity_o):
         raise ValueError("out's cache must be like the input's with at least keep rows a head")
     _check_int32(kept, "out's kept", heads * keep)
     _check_int32(lengths_o, "out's lengths", heads)
