@@ -8,9 +8,10 @@
 // CTA: one pass for the running (m, l) of every query, an exchange of the
 // kCluster partial (m, l) through distributed shared memory, and a second pass
 // that adds the weights (its scores come from L2).  4 G bytes per key are read
-// twice and 8 bytes of w moved once.  32 heads of 131072 keys, G = 4: 41 us, 2.4 TB/s of
+// twice and 8 bytes of w moved once.  32 heads of 131072 keys, G = 4: 38 us, 2.6 TB/s of
 // those 100 MB with the second reading from L2; bound by its instructions (issue 42 %, the
-// special function unit 40 % busy) and the two passes' latencies.  4-byte loads: 51 us.
+// special function unit 40 % busy) and the two passes' latencies.  4-byte loads: 51 us,
+// twice the scores in flight (one CTA an SM) 55 us, half of them in the second pass 41 us.
 //
 // Eviction of head h with len rows, of which the last `recent` stay anyway:
 // among t < len - recent the k = keep - recent rows of largest weight stay,
@@ -176,11 +177,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) wei
     }
     cluster.sync();                                           // no CTA leaves while its (m, l) are read
     float *dst = p.weights + static_cast<int64_t>(h) * p.capacity;
-    constexpr int U2 = U / 2;
-    for (int t = t0 + threadIdx.x * kVec; t < t1; t += U2 * kThreads * kVec) {
-        float v[U2][G][kVec], w[U2][kVec];
+    for (int t = t0 + threadIdx.x * kVec; t < t1; t += U * kThreads * kVec) {
+        float v[U][G][kVec], w[U][kVec];
 #pragma unroll
-        for (int u = 0; u < U2; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int at = t + u * kThreads * kVec;
 #pragma unroll
             for (int g = 0; g < G; ++g) load(g, at, v[u][g]);
@@ -192,7 +192,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) wei
             }
         }
 #pragma unroll
-        for (int u = 0; u < U2; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int at = t + u * kThreads * kVec;
 #pragma unroll
             for (int g = 0; g < G; ++g)
