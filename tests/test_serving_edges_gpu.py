@@ -45,6 +45,18 @@ def test_prompt_many_sequences(dtype, d, batch):
     _check_prompt(q, K, V, cu_q, cu_k, out, lse)
 
 
+@pytest.mark.parametrize("dtype,d", [(BF16, 64), (F16, 128)])
+@pytest.mark.parametrize("group", [2, 3, 5, 6, 7, 8])
+def test_prompt_even_and_odd_groups(dtype, d, group):
+    """Even groups go two heads at a time, odd ones 256 queries at a time: sequences that
+    end around 128 and 256, without keys, and with queries that see none."""
+    lens_q, lens_k = [129, 1, 0, 257, 128, 300], [129, 600, 40, 257, 0, 45]
+    cu_q, cu_k = _cu(lens_q), _cu(lens_k)
+    q, K, V = _prompt_inputs(dtype, d, 2, group, cu_q[-1], cu_k[-1], seed=group)
+    out, lse = axr.axr_prompt_attention(q, K, V, _int32(cu_q), _int32(cu_k))
+    _check_prompt(q, K, V, cu_q, cu_k, out, lse)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_prompt_broadcast_heads_and_no_keys(dtype):
     q, K, V = _prompt_inputs(dtype, 128, 3, 2, 140, 140, seed=2)
